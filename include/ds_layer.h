@@ -91,7 +91,8 @@ typedef enum {
   DS_ERR_DEVICE = 5         /* a device-side check failed (see ds_workspace_status) */
 } ds_status;
 
-typedef enum { DS_F16 = 0, DS_BF16 = 1, DS_I8 = 2 } ds_dtype;
+typedef enum { DS_F16 = 0, DS_BF16 = 1, DS_I8 = 2,
+               DS_U4 = 3 /* paged caches only: 4-bit codes with a scale and a minimum per row */ } ds_dtype;
 
 /* Shape and numeric format of one layer ([P1] §3.2; dtypes as in the [P3]
  * configuration table; int8 weights as in [P1] §5.2). */
@@ -392,6 +393,135 @@ DS_API ds_status ds_tp_ffn_partial(ds_tp_layer* layer, const float* x1, float* y
  * activation dtype (round to nearest even). */
 DS_API ds_status ds_tp_finish(ds_tp_layer* layer, const float* y, void* x_out, int rows, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged KV cache: keys and values of sequences of different lengths in pages
+ * that a table assigns, grouped query heads, rotary positions, and pages held
+ * in 16 bits or in 4.  The source pages keep one contiguous cache per sequence
+ * ([P1] §3.2 region 2); pages, rotation, grouped heads and 4-bit rows are this
+ * library's own extension of that region.
+ *
+ *   ds_paged_append     new keys and values into the pages, rotation on the way
+ *   ds_paged_gather     rows of the pages read back as packed values
+ *   ds_paged_attention  1 .. 16 new tokens per sequence over the pages
+ *   ds_prompt_attention whole prompts (or chunks of them), packed, causal
+ *
+ * Packed tensors hold the tokens of all sequences one after the other,
+ * [tokens][heads][head_dim]: the rows of sequence b are cu[b] .. cu[b+1]-1,
+ * with cu a DEVICE int32 array of batch + 1 non-decreasing entries, cu[0] = 0.
+ * A sequence may have no rows.  Rows behind cu[batch] belong to nobody: they
+ * are neither read nor written.  A packed tensor has a token stride in
+ * elements (a multiple of 8, at least heads * head_dim), so that q, k and v
+ * may be parts of one projection's rows; heads and channels are contiguous.
+ *
+ * Position p of sequence b is row p % page_size of page
+ * block_table[b][p / page_size].  Different sequences may read the same page
+ * (a shared prefix); a page that one call writes for one sequence may be
+ * written or read by no other sequence in that call.
+ *
+ * Query heads h of group h / (heads / kv_heads) read that key head; heads is
+ * a multiple of kv_heads.  head_dim is 64 or 128, page_size 16, 32, 64 or 128.
+ *
+ * Device-side checks: a position at or past table_stride * page_size, or past
+ * the rotation table, sets DS_DEVFLAG_CACHE_OVERFLOW; an entry of the table
+ * outside 0 .. num_pages-1 where a row is needed sets DS_DEVFLAG_BAD_PAGE.
+ * Such rows are not written (append: neither k, v nor q_out), not attended
+ * (attention), or read back as zeros (gather).  The flags are in the status
+ * word of `workspace` (ds_workspace_status).
+ *
+ * Every entry point returns DS_ERR_INVALID_ARG before any launch for pointers
+ * that are not memory of the current device.  tokens == 0 is valid: nothing
+ * is launched.  A workspace serves one call at a time: calls that may overlap
+ * (two streams, two replayed graphs) need one each.  All four calls can be
+ * captured into a CUDA graph. */
+typedef struct {
+  void *k, *v;        /* DEVICE pages [num_pages][kv_heads][page_size][head_dim] in act_dtype;
+                       * DS_U4: codes [num_pages][kv_heads][page_size][head_dim / 2], channel 2i
+                       * in the low and channel 2i+1 in the high four bits of byte i */
+  void *k_scale, *v_scale; /* DS_U4 only: float16 [num_pages][kv_heads][page_size][2], (scale, minimum)
+                            * of each row: value = code * scale + minimum */
+  const int32_t* block_table; /* DEVICE [batch][table_stride] page of each page_size positions */
+  int num_pages;
+  int page_size;      /* 16, 32, 64 or 128 */
+  int table_stride;   /* pages per sequence in block_table */
+  int kv_heads;
+  int head_dim;       /* 64 or 128 */
+  ds_dtype dtype;     /* what the pages hold: act_dtype or DS_U4 */
+  ds_dtype act_dtype; /* DS_F16 or DS_BF16: q, k, v and outputs */
+} ds_paged_cache;
+
+/* Rotary positions.  cos_sin: DEVICE float32 [max_pos][rotary_dim]; row p
+ * holds the cosines of the rotary_dim / 2 angles of position p, then their
+ * sines (the caller's table, so that any base or scaling of positions works).
+ * The first rotary_dim channels of a head are rotated, (x1, x2) ->
+ * (x1 cos - x2 sin, x2 cos + x1 sin), the rest pass: pair i is channels
+ * (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved = 1. */
+typedef struct {
+  const float* cos_sin;
+  int max_pos;
+  int rotary_dim;  /* a multiple of 16, 16 .. head_dim */
+  int interleaved; /* 0 or 1 */
+} ds_rotary;
+
+/* Appends packed k and v [tokens][kv_heads][head_dim] to the pages: row t of
+ * sequence b goes to position past_len[b] + t - cu_seqlens[b].  With `rotary`
+ * (else null) k, and q if given, are rotated by that position in fp32, and
+ * rounded once.  q [tokens][heads][head_dim] -> q_out (may be q itself with
+ * the same stride; q null: heads, q_out and their strides are ignored).
+ * DS_U4 rows are quantised from the rotated fp32 values: m = fp16(min),
+ * s = fp16((max - m) / 15), code = clamp(rne((x - m) / s), 0, 15), 0 where
+ * s = 0 (float32, round to nearest even); a row with a value that is not
+ * finite, or beyond fp16's range, reads back as values that are not finite.
+ * past_len [batch] DEVICE int32, not advanced; rows at negative positions are
+ * skipped.  workspace: any workspace of 256 bytes or more (status word). */
+DS_API ds_status ds_paged_append(const ds_paged_cache* cache, const ds_rotary* rotary, const void* q, void* q_out,
+                                 int heads, const void* k, const void* v, int64_t q_stride, int64_t q_out_stride,
+                                 int64_t k_stride, int64_t v_stride, int tokens, const int32_t* cu_seqlens,
+                                 const int32_t* past_len, int batch, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/* Reads rows of the pages back: row t of sequence b of k_out and v_out
+ * [tokens][kv_heads][head_dim] (act_dtype; DS_U4 rows as code * scale +
+ * minimum, rounded once) is position first_pos[b] + t - cu_seqlens[b]; rows
+ * at negative positions are left as they are.  workspace as for the append. */
+DS_API ds_status ds_paged_gather(const ds_paged_cache* cache, void* k_out, void* v_out, int64_t k_stride,
+                                 int64_t v_stride, int tokens, const int32_t* cu_seqlens, const int32_t* first_pos,
+                                 int batch, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of ds_paged_attention on the current device; 0 for
+ * invalid arguments.  Zero-filled once (ds_workspace_init). */
+DS_API size_t ds_paged_attention_workspace_bytes(const ds_paged_cache* cache, int heads, int batch, int new_tokens);
+
+/* Attention of T = new_tokens (1 .. 16) new tokens per sequence over the
+ * pages, which already hold the new tokens' keys and values (ds_paged_append):
+ * row b T + t of q [batch T][heads][head_dim] attends positions 0 ..
+ * past_len[b] + t, out = softmax(scale q K^T) V.  A row that sees no position
+ * (past_len[b] + t < 0: an idle slot of a padded batch) is written as zeros.
+ * Positions past past_len[b] + T - 1 are never read.  out must not alias q.
+ * fp32 softmax and sums; the softmax weights are rounded to the type of the
+ * values (DS_U4: to fp16, after the row's scale) for the product with them. */
+DS_API ds_status ds_paged_attention(const ds_paged_cache* cache, const void* q, void* out, int heads,
+                                    int64_t q_stride, int64_t out_stride, const int32_t* past_len, int batch,
+                                    int new_tokens, float scale, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of ds_prompt_attention for packed q of `tokens` rows. */
+DS_API size_t ds_prompt_attention_workspace_bytes(int heads, int batch, int tokens);
+
+/* Causal attention over packed prompts: sequence b has Lq = cu_q[b+1] -
+ * cu_q[b] queries and Lk = cu_k[b+1] - cu_k[b] keys; query i sees keys
+ * j <= Lk - Lq + i (the queries are the last Lq positions: Lk = Lq is a whole
+ * prompt, Lk > Lq a chunk on top of cached keys, which ds_paged_gather reads
+ * back).  A query that sees no key (Lk < Lq) is written as zeros.
+ *   q, out [q_tokens][heads][head_dim], k, v [k_tokens][kv_heads][head_dim],
+ *   in act_dtype; out must not alias an input.
+ * fp32 softmax and sums; the softmax weights are rounded to act_dtype for the
+ * product with v.  A value of k or v that is not finite can reach every row of
+ * its own sequence, masked or not, and no other sequence. */
+DS_API ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void* out, int heads, int kv_heads,
+                                     int head_dim, ds_dtype act_dtype, int64_t q_stride, int64_t k_stride,
+                                     int64_t v_stride, int64_t out_stride, int q_tokens, int k_tokens,
+                                     const int32_t* cu_q, const int32_t* cu_k, int batch, float scale,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
 /* Device-side status flags recorded in the workspace. */
 #define DS_DEVFLAG_CACHE_OVERFLOW 0x1  /* past_len[b] + T > max_len for some row */
 #define DS_DEVFLAG_WAIT_TIMEOUT 0x2    /* an in-kernel pipeline wait gave up (outputs invalid) */
@@ -399,6 +529,8 @@ DS_API ds_status ds_tp_finish(ds_tp_layer* layer, const float* y, void* x_out, i
                                         * libdslayer_debug_bounds.so): a kernel found an index
                                         * outside its buffer and skipped the access (outputs
                                         * invalid); normal builds compile the checks away */
+
+#define DS_DEVFLAG_BAD_PAGE 0x8        /* a block table entry outside 0 .. num_pages-1 was needed */
 
 /* Copies the workspace status word to *flags_out, clears it, and synchronises
  * `stream`.  Returns DS_ERR_DEVICE when a flag was set, DS_OK otherwise. */

@@ -20,7 +20,10 @@ quant   MoQ-style symmetric per-group int8 quantisation and dequantisation.
 moe     the residual-MoE (PR-MoE) FFN block with top-1 routing.
 tp      the tensor-sliced (Megatron-style) layer: shards, per-rank partial
         sums and their reduction.
+paged   the paged-cache operators: rotation, 4-bit rows, attention over pages
+        and over packed prompts.
 """
+from . import paged
 from .layer import (layer_norm, linear, gelu_tanh, softmax, decode_attention,
                     layer_forward, stack_forward, LAYER_PARAM_NAMES)
 from .quant import quantize_int8, dequantize_int8, fp16_scale_from_amax
@@ -32,4 +35,5 @@ __all__ = [
     "layer_forward", "stack_forward", "LAYER_PARAM_NAMES",
     "quantize_int8", "dequantize_int8", "fp16_scale_from_amax", "ffn", "residual_moe_ffn",
     "shard_layer_params", "tp_attention_partial", "tp_ffn_partial", "tp_layer_forward",
+    "paged",
 ]

@@ -1,0 +1,202 @@
+"""The paged-cache operators without a device: what the oracle must satisfy,
+and the calls that are refused before any device is touched."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as op
+from test_abi import lib  # noqa: F401  (fixture)
+from transformer_layer_gb300 import ds
+
+P = C.c_void_p(4096)  # an aligned pointer that is never read
+
+
+# ---------------------------------------------------------------- oracle pins
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_is_a_rotation(inter):
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((3, 2, 64))
+    th = rng.uniform(0, 6, 16)
+    cs = np.concatenate([np.cos(th), np.sin(th)])
+    y = op.rotate(x, cs, inter)
+    assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1), rtol=1e-13)
+    assert np.array_equal(y[..., 32:], x[..., 32:])          # channels behind the rotated ones pass
+    back = op.rotate(y, np.concatenate([np.cos(-th), np.sin(-th)]), inter)
+    assert np.allclose(back, x, rtol=1e-12, atol=1e-13)
+    # a quarter turn sends (1, 0) to (0, 1)
+    e = np.zeros(64)
+    e[0] = 1
+    quarter = np.concatenate([np.zeros(16), np.ones(16)])
+    assert op.rotate(e, quarter, inter)[1 if inter else 16] == 1
+
+
+def test_rotated_scores_depend_on_the_distance_only():
+    rng = np.random.default_rng(2)
+    q, k = rng.standard_normal(64), rng.standard_normal(64)
+    freq = 10000.0 ** (-np.arange(32) / 32)
+
+    def at(x, p):
+        return op.rotate(x, np.concatenate([np.cos(p * freq), np.sin(p * freq)]))
+    assert abs(at(q, 17) @ at(k, 5) - at(q, 112) @ at(k, 100)) < 1e-11
+
+
+def test_u4_rows():
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((50, 128)).astype(np.float32)
+    c, sc = op.quantize_u4(x)
+    y = op.dequantize_u4(op.pack_u4(c), sc)
+    s = sc[:, :1].astype(np.float64)
+    # half a step, and what rounding the minimum and 15 steps to fp16 can add
+    assert np.all(np.abs(y - x) <= s / 2 + (np.abs(x).max(-1, keepdims=True) + 16 * s) * 2.0 ** -10)
+    assert c.max() == 15 and c.min() == 0
+    assert np.array_equal(op.unpack_u4(op.pack_u4(c)), c)
+    # integers 0 .. 15 are exact; an equal row has scale 0 and reads back as its value
+    z = np.tile(np.arange(16, dtype=np.float32), 4)[None]
+    c, sc = op.quantize_u4(z)
+    assert np.array_equal(op.dequantize_u4(op.pack_u4(c), sc), z)
+    c, sc = op.quantize_u4(np.full((1, 64), 3.5, np.float32))
+    assert sc[0, 0] == 0 and np.all(op.dequantize_u4(op.pack_u4(c), sc) == 3.5)
+
+
+def test_attend_closed_forms():
+    rng = np.random.default_rng(4)
+    v = rng.standard_normal((5, 1, 4))
+    out, _ = op.attend(np.zeros((5, 2, 4)), rng.standard_normal((5, 1, 4)), v, 1, 0.5)
+    for i in range(5):  # equal scores: the mean of the values seen
+        assert np.allclose(out[i], v[:i + 1].mean(0), rtol=1e-14)
+    # a query before the first key sees nothing
+    out, _ = op.attend(np.ones((3, 1, 4)), np.ones((1, 1, 4)), v[:1], 1 - 3 + 1, 1.0)
+    assert np.all(out[:2] == 0) and np.allclose(out[2], v[0])
+    # pages hold the same rows as the packed form, whatever order they are in
+    k, v = rng.standard_normal((40, 2, 8)), rng.standard_normal((40, 2, 8))
+    q = rng.standard_normal((3, 4, 8))
+    table = np.array([[2, 0, 1]])
+    kp, vp = np.full((3, 2, 16, 8), np.nan), np.full((3, 2, 16, 8), np.nan)
+    for p in range(40):
+        pg, r = op.place(table, 16, 0, p)
+        kp[pg, :, r], vp[pg, :, r] = k[p], v[p]
+    a, _ = op.paged_attention(q, kp, vp, table, 16, [37], 3, 0.3)
+    b, _ = op.prompt_attention(q, k, v, [0, 3], [0, 40], 0.3)
+    assert np.allclose(a, b, rtol=1e-13)
+
+
+# ---------------------------------------------------------------- refusals
+def cache(**kw):
+    f = dict(k=P, v=P, k_scale=P, v_scale=P, block_table=P, num_pages=4, page_size=16, table_stride=2, kv_heads=2,
+             head_dim=64, dtype=ds.DS_F16, act_dtype=ds.DS_F16)
+    f.update(kw)
+    return ds.ds_paged_cache(**f)
+
+
+BAD_CACHES = [
+    (dict(act_dtype=ds.DS_I8, dtype=ds.DS_I8), ds.DS_ERR_INVALID_ARG), (dict(dtype=ds.DS_I8), ds.DS_ERR_UNSUPPORTED),
+    (dict(dtype=ds.DS_BF16), ds.DS_ERR_UNSUPPORTED), (dict(head_dim=96), ds.DS_ERR_UNSUPPORTED),
+    (dict(page_size=8), ds.DS_ERR_UNSUPPORTED), (dict(page_size=24), ds.DS_ERR_UNSUPPORTED),
+    (dict(page_size=256), ds.DS_ERR_UNSUPPORTED), (dict(num_pages=0), ds.DS_ERR_INVALID_ARG),
+    (dict(table_stride=0), ds.DS_ERR_INVALID_ARG), (dict(table_stride=1 << 28), ds.DS_ERR_UNSUPPORTED),
+    (dict(kv_heads=0), ds.DS_ERR_INVALID_ARG), (dict(k=None), ds.DS_ERR_INVALID_ARG),
+    (dict(v=C.c_void_p(4104)), ds.DS_ERR_INVALID_ARG), (dict(block_table=None), ds.DS_ERR_INVALID_ARG),
+    (dict(dtype=ds.DS_U4, k_scale=None), ds.DS_ERR_INVALID_ARG),
+]
+
+
+def append(lib, c, **kw):  # noqa: F811
+    a = dict(rot=None, q=P, q_out=P, heads=2, k=P, v=P, qs=128, qos=128, ks=128, vs=128, tokens=3, cu=P, past=P, batch=2,
+             ws=P, ws_bytes=256)
+    a.update(kw)
+    return lib.ds_paged_append(C.byref(c) if c is not None else None, C.byref(a["rot"]) if a["rot"] else None, a["q"],
+                               a["q_out"], a["heads"], a["k"], a["v"], a["qs"], a["qos"], a["ks"], a["vs"], a["tokens"],
+                               a["cu"], a["past"], a["batch"], a["ws"], a["ws_bytes"], None)
+
+
+def attention(lib, c, **kw):  # noqa: F811
+    a = dict(q=P, out=C.c_void_p(8192), heads=4, qs=256, os=256, past=P, batch=2, T=1, scale=0.1, ws=P, ws_bytes=1 << 30)
+    a.update(kw)
+    return lib.ds_paged_attention(C.byref(c) if c is not None else None, a["q"], a["out"], a["heads"], a["qs"], a["os"],
+                                  a["past"], a["batch"], a["T"], a["scale"], a["ws"], a["ws_bytes"], None)
+
+
+def prompt(lib, **kw):  # noqa: F811
+    a = dict(q=P, k=P, v=P, out=C.c_void_p(8192), heads=4, kv=2, d=64, dt=ds.DS_F16, qs=256, ks=128, vs=128, os=256, nq=5,
+             nk=5, cu_q=P, cu_k=P, batch=2, scale=0.1, ws=P, ws_bytes=1 << 30)
+    a.update(kw)
+    return lib.ds_prompt_attention(a["q"], a["k"], a["v"], a["out"], a["heads"], a["kv"], a["d"], a["dt"], a["qs"], a["ks"],
+                                   a["vs"], a["os"], a["nq"], a["nk"], a["cu_q"], a["cu_k"], a["batch"], a["scale"],
+                                   a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_bad_caches_are_refused_by_every_call(lib, kw, code):  # noqa: F811
+    c = cache(**kw)
+    assert append(lib, c) == code and lib.ds_last_error()
+    assert lib.ds_paged_gather(C.byref(c), P, P, 128, 128, 3, P, P, 2, P, 256, None) == code
+    assert attention(lib, c) == code
+    assert lib.ds_paged_attention_workspace_bytes(C.byref(c), 4, 2, 1) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), ds.DS_ERR_INVALID_ARG), (dict(v=C.c_void_p(4098)), ds.DS_ERR_INVALID_ARG),
+    (dict(ks=64), ds.DS_ERR_INVALID_ARG), (dict(vs=132), ds.DS_ERR_INVALID_ARG), (dict(qs=64), ds.DS_ERR_INVALID_ARG),
+    (dict(qos=192), ds.DS_ERR_INVALID_ARG),                       # in place with two strides
+    (dict(heads=0), ds.DS_ERR_INVALID_ARG), (dict(q_out=None), ds.DS_ERR_INVALID_ARG),
+    (dict(tokens=-1), ds.DS_ERR_INVALID_ARG), (dict(batch=0), ds.DS_ERR_INVALID_ARG), (dict(cu=None), ds.DS_ERR_INVALID_ARG),
+    (dict(past=C.c_void_p(4098)), ds.DS_ERR_INVALID_ARG), (dict(ws=C.c_void_p(4112)), ds.DS_ERR_INVALID_ARG),
+    (dict(ws_bytes=128), ds.DS_ERR_WORKSPACE), (dict(rot=ds.ds_rotary(None, 10, 64, 0)), ds.DS_ERR_INVALID_ARG),
+    (dict(rot=ds.ds_rotary(4096, 0, 64, 0)), ds.DS_ERR_INVALID_ARG), (dict(rot=ds.ds_rotary(4096, 10, 72, 0)), ds.DS_ERR_UNSUPPORTED),
+    (dict(rot=ds.ds_rotary(4096, 10, 80, 0)), ds.DS_ERR_UNSUPPORTED), (dict(rot=ds.ds_rotary(4096, 10, 64, 2)), ds.DS_ERR_INVALID_ARG),
+])
+def test_append_refusals(lib, kw, code):  # noqa: F811
+    assert append(lib, cache(), **kw) == code, lib.ds_last_error()
+    assert append(lib, None) == ds.DS_ERR_INVALID_ARG
+    assert append(lib, cache(), tokens=0) == ds.DS_OK             # nothing to do, no device needed
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(heads=3), ds.DS_ERR_INVALID_ARG), (dict(heads=0), ds.DS_ERR_INVALID_ARG), (dict(batch=0), ds.DS_ERR_INVALID_ARG),
+    (dict(batch=1 << 17), ds.DS_ERR_INVALID_ARG), (dict(T=0), ds.DS_ERR_UNSUPPORTED), (dict(T=17), ds.DS_ERR_UNSUPPORTED),
+    (dict(scale=float("inf")), ds.DS_ERR_INVALID_ARG), (dict(scale=float("nan")), ds.DS_ERR_INVALID_ARG),
+    (dict(q=None), ds.DS_ERR_INVALID_ARG), (dict(out=P), ds.DS_ERR_INVALID_ARG), (dict(qs=255), ds.DS_ERR_INVALID_ARG),
+    (dict(os=128), ds.DS_ERR_INVALID_ARG), (dict(past=None), ds.DS_ERR_INVALID_ARG),
+])
+def test_attention_refusals(lib, kw, code):  # noqa: F811
+    assert attention(lib, cache(), **kw) == code, lib.ds_last_error()
+    assert attention(lib, None) == ds.DS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=ds.DS_I8), ds.DS_ERR_INVALID_ARG), (dict(dt=ds.DS_U4), ds.DS_ERR_INVALID_ARG), (dict(d=80), ds.DS_ERR_UNSUPPORTED),
+    (dict(heads=5), ds.DS_ERR_INVALID_ARG), (dict(kv=0), ds.DS_ERR_INVALID_ARG), (dict(nq=-1), ds.DS_ERR_INVALID_ARG),
+    (dict(nk=-1), ds.DS_ERR_INVALID_ARG), (dict(nq=1 << 25), ds.DS_ERR_INVALID_ARG), (dict(cu_q=None), ds.DS_ERR_INVALID_ARG),
+    (dict(cu_k=C.c_void_p(4097)), ds.DS_ERR_INVALID_ARG), (dict(batch=0), ds.DS_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), ds.DS_ERR_INVALID_ARG), (dict(q=None), ds.DS_ERR_INVALID_ARG), (dict(k=None), ds.DS_ERR_INVALID_ARG),
+    (dict(out=P), ds.DS_ERR_INVALID_ARG), (dict(ks=120), ds.DS_ERR_INVALID_ARG), (dict(os=260), ds.DS_ERR_INVALID_ARG),
+    (dict(ws=None), ds.DS_ERR_INVALID_ARG), (dict(ws_bytes=64), ds.DS_ERR_WORKSPACE),
+])
+def test_prompt_refusals(lib, kw, code):  # noqa: F811
+    assert prompt(lib, **kw) == code, lib.ds_last_error()
+    assert prompt(lib, nq=0) == ds.DS_OK
+    assert lib.ds_prompt_attention_workspace_bytes(0, 1, 1) == 0
+    assert lib.ds_prompt_attention_workspace_bytes(1, 1, -1) == 0
+
+
+def test_binding_checks_its_tensors():
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
+    table = torch.zeros(2, 2, dtype=torch.int32)
+    c = ds.paged_cache(k, k.clone(), table, torch.float16)
+    assert (c.num_pages, c.kv_heads, c.page_size, c.head_dim, c.table_stride, c.dtype) == (4, 2, 16, 64, 2, ds.DS_F16)
+    codes = torch.zeros(4, 2, 16, 32, dtype=torch.uint8)
+    sc = torch.zeros(4, 2, 16, 2, dtype=torch.float16)
+    c4 = ds.paged_cache(codes, codes.clone(), table, torch.bfloat16, sc, sc.clone())
+    assert (c4.head_dim, c4.dtype, c4.act_dtype) == (64, ds.DS_U4, ds.DS_BF16)
+    for bad in (lambda: ds.paged_cache(k, k.transpose(1, 2), table, torch.float16),
+                lambda: ds.paged_cache(k, k, table.long(), torch.float16),
+                lambda: ds.paged_cache(codes, codes, table, torch.float16),
+                lambda: ds.paged_cache(k[0], k[0], table, torch.float16),
+                lambda: ds.rotary(torch.zeros(5, 64, dtype=torch.float64)),
+                lambda: ds.ds_paged_attention(c, k[0], k[0], table[0], 1, 1, table, 256),       # wrong row count
+                lambda: ds.ds_paged_attention(c, k[0, :, :3], k[0, :, :3], table[0], 3, 1, table, 256),
+                lambda: ds.ds_paged_gather(c, k[0], k[0], table[0], table[0].long(), 1, table)):
+        with pytest.raises((ValueError, KeyError)):
+            bad()

@@ -1,0 +1,562 @@
+"""GPU parity of the paged-cache operators against the float64 oracle.
+
+Tolerances, elementwise, derived before the first run.  u = eps / 2 of the
+output type (one rounding), w = eps / 2 of the type the softmax weights are
+rounded to for the product with V (the activation type; fp16 for 4-bit pages),
+A = sum_j p_j |v_j| from the oracle.  Then
+  |out - ref| <= u (|ref| + w A) + w A + f A + tiny,
+where f bounds the fp32 steps: a score of d products is off by at most
+(d + 4) 2^-24 max_j sum |q||k_j| scale log2(e), in units where a weight moves
+by ln 2 a unit, twice (weight and sum); exp2 by 2 ulps; the two sums over n
+weights by n 2^-24 each; joining parts by 64 2^-24.  tiny covers weights that
+fall below the 16-bit type's normal range: 2^-25 of the largest weight, n
+times, times the largest |v|.  4-bit pages: the query is scaled by a power of
+two and held in fp16, off by at most 2^-20 of its largest channel; the weights
+carry the row's scale, so A is summed over code * scale + |minimum|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from helpers import new_workspace, to64
+from oracle import paged as op
+from transformer_layer_gb300 import ds
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(shape, g, dtype):
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def starts(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+
+
+def strided(rows, heads, d, dtype, extra=24):
+    """A packed tensor whose rows lie further apart than they are long."""
+    return torch.full((rows, heads * d + extra), float("nan"), dtype=dtype, device="cuda")[:, :heads * d].view(rows, heads, d) \
+        if extra == 0 else torch.as_strided(torch.full((max(rows, 1) * (heads * d + extra),), float("nan"), dtype=dtype, device="cuda"),
+                                            (rows, heads, d), (heads * d + extra, d, 1))
+
+
+class Pages:
+    """Pages whose unowned rows are NaN (4-bit: NaN scales), owned rows random."""
+
+    def __init__(self, lens, page, nk, d, dtype, u4, seed, spare=2):
+        g = gen(seed)
+        need = [-(-max(0, n) // page) for n in lens]
+        self.page, self.nk, self.d, self.dtype, self.u4 = page, nk, d, dtype, u4
+        total = sum(need) + spare
+        order = torch.randperm(total, generator=torch.Generator().manual_seed(seed)).numpy()
+        self.table = np.full((len(lens), max(max(need), 1) + 1), -1, np.int64)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        own = np.zeros((total, page), bool)
+        for b, n in enumerate(lens):
+            for p in range(max(0, n)):
+                pg, r = op.place(self.table, page, b, p)
+                own[pg, r] = True
+        own = torch.tensor(own, device="cuda")[:, None, :, None]
+        self.k_scale = self.v_scale = None
+        if u4:
+            self.k, self.v = (torch.randint(0, 256, (total, nk, page, d // 2), generator=g, device="cuda", dtype=torch.uint8)
+                              for _ in range(2))
+            self.k_scale, self.v_scale = (
+                torch.where(own, torch.cat([torch.rand((total, nk, page, 1), generator=g, device="cuda") * 0.3 + 0.01,
+                                            -torch.rand((total, nk, page, 1), generator=g, device="cuda") * 2], -1),
+                            float("nan")).half() for _ in range(2))
+        else:
+            self.k, self.v = (torch.where(own, torch.randn((total, nk, page, d), generator=g, device="cuda"),
+                                          float("nan")).to(dtype) for _ in range(2))
+        self.t = i32(self.table)
+        self.handle = ds.paged_cache(self.k, self.v, self.t, dtype, self.k_scale, self.v_scale)
+
+    def values(self):
+        if self.u4:
+            return [op.dequantize_u4(c.cpu().numpy(), s.cpu().numpy()) for c, s in ((self.k, self.k_scale), (self.v, self.v_scale))]
+        return [to64(self.k), to64(self.v)]
+
+    def magnitudes(self):
+        """|v| as the weights multiply it: |value|, for 4-bit rows code * scale + |minimum|."""
+        if not self.u4:
+            return np.abs(to64(self.v))
+        s = self.v_scale.double().cpu().numpy()
+        return op.unpack_u4(self.v.cpu().numpy()) * s[..., :1] + np.abs(s[..., 1:])
+
+
+def status_ok(ws):
+    code, flags = ds.ds_workspace_status(ws)
+    assert code == ds.DS_OK and flags == 0, flags
+
+
+def check(out, ref, A, vmax, qk, q_max, n, d, scale, dtype, w, u4=False, what=""):
+    """qk: largest sum |q||k| of a score; vmax: largest |v|; n: keys."""
+    o = to64(out)
+    u = half_step(dtype)
+    e = 2.0 ** -24
+    f = 2 * np.log(2) * ((d + 4) * e * qk * scale * 1.4427 + (2.0 ** -20 * q_max * np.sqrt(d) * scale * 40 if u4 else 0)) \
+        + 2 * 4 * e + 2 * n * e + 64 * e
+    tol = u * (np.abs(ref) + w * A) + w * A + f * A + 2.0 ** -25 * n * vmax * 0.01 + 2.0 ** -25
+    err = np.abs(o - ref)
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{what}: worst {np.nanmax(err / tol):.2f} of the tolerance, {bad.sum()} of {bad.size}, " \
+                          f"first at {np.argwhere(bad)[0]}"
+
+
+# ---------------------------------------------------------------- append, gather
+def table_of(max_pos, r):
+    a = np.arange(max_pos)[:, None] * 10000.0 ** (-np.arange(r // 2) / (r // 2))
+    return torch.tensor(np.concatenate([np.cos(a), np.sin(a)], 1), dtype=torch.float32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype,u4,page,nk,G,d,r,inter,new,past", [
+    (F16, False, 16, 2, 2, 64, 64, False, [1], [0]),
+    (F16, False, 16, 1, 3, 128, 128, False, [1, 1, 1], [5, 16, 31]),
+    (BF16, False, 32, 3, 1, 128, 64, True, [7, 0, 33, 1], [0, 9, 31, 64]),
+    (BF16, False, 128, 2, 5, 64, 32, False, [130, 1], [127, 3]),
+    (F16, False, 64, 8, 4, 128, 0, False, [70, 3], [1, 64]),
+    (F16, True, 16, 2, 2, 64, 64, False, [1, 17, 0, 40], [15, 3, 7, 0]),
+    (BF16, True, 32, 5, 3, 128, 128, True, [3, 65], [30, 0]),
+    (BF16, True, 64, 1, 1, 128, 48, False, [1] * 40, list(range(40))),
+    (F16, True, 128, 3, 0, 128, 16, True, [300], [40]),
+])
+def test_append_and_gather(dtype, u4, page, nk, G, d, r, inter, new, past):
+    B, N = len(new), sum(new)
+    lens = [a + b for a, b in zip(new, past)]
+    c = Pages(lens, page, nk, d, dtype, u4, 11)
+    before = c.values()
+    nh = nk * G
+    g = gen(5)
+    pad = 3  # rows behind the last sequence
+    q, k, v = (strided(N + pad, h, d, dtype).copy_(randn((N + pad, h, d), g, dtype)) for h in (max(nh, 1), nk, nk))
+    q_out = strided(N + pad, max(nh, 1), d, dtype, 8)
+    cu = starts(new)
+    tab = table_of(max(lens) + 1, r) if r else None
+    ws = new_workspace(256)
+    n0 = ds.ds_launch_count()
+    ds.ds_paged_append(c.handle, q if G else None, k, v, q_out if G else None, i32(cu), i32(past), B,
+                       ds.rotary(tab, inter) if r else None, ws)
+    assert ds.ds_launch_count() == n0 + 1
+    status_ok(ws)
+    # what every row must hold
+    u, e = half_step(dtype), 2.0 ** -24
+    tab64 = to64(tab) if r else None
+    after = c.values()
+    want = [x.copy() for x in before]
+    tol = [np.zeros_like(x) for x in before]
+    for t, b, pos in op.positions(cu, past):
+        pg, row = op.place(c.table, page, b, pos)
+        rows = [to64(x[t]) for x in (k, v)]
+        if r:
+            rows[0] = op.rotate(rows[0], tab64[pos], inter)
+            if G:
+                ref = op.rotate(to64(q[t]), tab64[pos], inter)
+                mag = np.abs(to64(q[t])).max() * 2
+                assert np.all(np.abs(to64(q_out[t]) - ref) <= u * np.abs(ref) + 4 * e * mag + 2.0 ** -25), (t, "q")
+        elif G:
+            assert torch.equal(q_out[t], q[t])
+        for i, x in enumerate(rows):
+            mag = np.abs(x).max(-1, keepdims=True)
+            if u4:
+                s = (x.max(-1, keepdims=True) - x.min(-1, keepdims=True)) / 15
+                # half a step, the minimum's and 15 steps' rounding to fp16, and a step where a tie falls the other way
+                want[i][pg, :, row] = x
+                tol[i][pg, :, row] = s / 2 * (1 + 2.0 ** -10) + (mag + 16 * s) * 2.0 ** -10 + 2.0 ** -24
+            else:
+                want[i][pg, :, row] = x
+                tol[i][pg, :, row] = u * np.abs(x) + 4 * e * mag * 2 + 2.0 ** -25 if (r and i == 0) else 0
+    for i in range(2):
+        same = np.isnan(want[i]) & np.isnan(after[i])  # rows nobody owns stay as they were
+        assert np.all(same | (np.abs(after[i] - want[i]) <= tol[i])), ("k", "v")[i]
+        if u4:  # rows that no token went to keep their bits
+            assert np.array_equal(after[i][tol[i] == 0], before[i][tol[i] == 0], equal_nan=True)
+    if G:
+        assert torch.isnan(q_out[N:]).all()
+    # reading back gives the rows' values, rounded once
+    ko, vo = strided(N + pad, nk, d, dtype), strided(N + pad, nk, d, dtype, 0)
+    ds.ds_paged_gather(c.handle, ko, vo, i32(cu), i32(past), B, ws)
+    status_ok(ws)
+    for t, b, pos in op.positions(cu, past):
+        pg, row = op.place(c.table, page, b, pos)
+        for i, x in enumerate((ko, vo)):
+            y = after[i][pg, :, row]
+            assert np.all(np.abs(to64(x[t]) - y) <= (u * np.abs(y) + e * np.abs(y) * 2 + 2.0 ** -25 if u4 else 0))
+    assert torch.isnan(ko[N:]).all() and torch.isnan(vo[N:]).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_u4_codes_are_the_definitions(dtype):
+    """Without rotation the quantiser's decisions are float32 ones: equal bits."""
+    nk, d, page = 3, 128, 16
+    c = Pages([50], page, nk, d, dtype, True, 3)
+    g = gen(9)
+    k, v = randn((50, nk, d), g, dtype), randn((50, nk, d), g, dtype) * 3
+    v[7] = 0.25  # a row without spread
+    ws = new_workspace(256)
+    ds.ds_paged_append(c.handle, None, k, v, None, i32([0, 50]), i32([0]), 1, None, ws)
+    for x, codes, scale in ((k, c.k, c.k_scale), (v, c.v, c.v_scale)):
+        want, sc = op.quantize_u4(x.float().cpu().numpy())
+        got, gs = codes.cpu().numpy(), scale.cpu().numpy()
+        for p in range(50):
+            pg, r = op.place(c.table, page, 0, p)
+            assert np.array_equal(gs[pg, :, r], sc[p]) and np.array_equal(got[pg, :, r], op.pack_u4(want[p])), p
+
+
+def test_append_in_place_and_rows_without_a_place():
+    """q rotated in place; a position past the pages, past the rotation table, a bad
+    page and a negative position write nothing (the first three raise a flag)."""
+    nk, d, page = 2, 64, 16
+    c = Pages([40, 40, 40, 40], page, nk, d, F16, False, 4)
+    tab = table_of(40, d)
+    g = gen(2)
+    end = c.table.shape[1] * page  # the table's last entry, and what lies behind it
+    for past, flag, bad in (([3, end, 5, 6], ds.DS_DEVFLAG_CACHE_OVERFLOW, 1), ([3, end - 1, 5, 6], ds.DS_DEVFLAG_BAD_PAGE, 1), ([3, 4, 40, 6], ds.DS_DEVFLAG_CACHE_OVERFLOW, 2),
+                            ([3, 4, 5, 6], ds.DS_DEVFLAG_BAD_PAGE, 3), ([-1, 4, 5, 6], 0, 0)):
+        tb = c.table.copy()
+        if bad == 3:
+            tb[bad, 0] = c.k.shape[0]
+        h = ds.paged_cache(c.k, c.v, i32(tb), F16)
+        q, k, v = (randn((4, n, d), g, F16) for n in (4, nk, nk))
+        q0, kc, vc = q.clone(), c.k.clone(), c.v.clone()
+        ws = new_workspace(256)
+        ds.ds_paged_append(h, q, k, v, q, i32([0, 1, 2, 3, 4]), i32(past), 4, ds.rotary(tab), ws)
+        code, flags = ds.ds_workspace_status(ws)
+        assert flags == flag
+        assert torch.equal(q[bad], q0[bad])
+        changed = (c.k != kc) & ~(torch.isnan(c.k) & torch.isnan(kc))
+        assert int(changed.flatten(1).any(1).sum()) <= 3
+        for b in range(4):
+            if b != bad:
+                ref = op.rotate(to64(q0[b]), to64(tab[past[b]]))
+                assert np.abs(to64(q[b]) - ref).max() < 2.0 ** -11 * 8
+
+
+# ---------------------------------------------------------------- attention over pages
+ATTN = [
+    # dtype, u4, page, nk, G, d, T, lens (new tokens included; <= 0: an idle slot)
+    (F16, False, 16, 1, 1, 64, 1, [1]),
+    (F16, False, 16, 2, 4, 128, 1, [1, 15, 16, 17, 33, 0, 250]),
+    (BF16, False, 32, 1, 8, 128, 1, [700, 31, 1]),
+    (BF16, False, 64, 5, 5, 64, 3, [64, 3, 129, 2, 700]),
+    (F16, False, 128, 2, 1, 128, 16, [16, 128, 300, 5, 1000]),
+    (BF16, False, 16, 1, 24, 128, 1, [90, 257]),
+    (F16, False, 16, 3, 3, 64, 7, [2049, 7, 8]),
+    (F16, False, 32, 8, 1, 128, 1, [5000]),
+    (F16, True, 16, 1, 1, 64, 1, [1]),
+    (F16, True, 16, 2, 4, 128, 1, [1, 15, 16, 17, 33, 0, 250]),
+    (BF16, True, 32, 1, 8, 128, 1, [700, 31, 1]),
+    (BF16, True, 64, 5, 5, 64, 3, [64, 3, 129, 2, 700]),
+    (F16, True, 128, 2, 1, 128, 16, [16, 128, 300, 5, 1000]),
+    (BF16, True, 16, 1, 24, 128, 1, [90, 257]),
+    (F16, True, 16, 3, 3, 64, 7, [2049, 7, 8]),
+    (BF16, True, 64, 4, 2, 128, 1, [9000, 1, 60]),
+    (BF16, False, 16, 2, 2, 64, 1, list(range(1, 130))),
+]
+
+
+def run_attention(c, q, lens, T, ws=None, out=None, scale=None, stream=None, heads=None):
+    B, nh = len(lens), q.shape[1]
+    past = i32([n - T for n in lens])
+    nb = ds.ds_paged_attention_workspace_bytes(c.handle, nh, B, T)
+    assert nb >= 256
+    ws = new_workspace(nb) if ws is None else ws
+    out = strided(B * T, nh, c.d, c.dtype, 16) if out is None else out
+    ds.ds_paged_attention(c.handle, q, out, past, B, T, ws, nb, scale, stream)
+    return out, ws
+
+
+def check_attention(c, q, out, lens, T, scale, what=""):
+    k, v = c.values()
+    k64, v64, m64 = np.nan_to_num(k), np.nan_to_num(v), np.nan_to_num(c.magnitudes())
+    q64 = to64(q)
+    past = [n - T for n in lens]
+    ref, _ = op.paged_attention(q64, k64, v64, c.table, c.page, past, T, scale)
+    A, _ = op.paged_attention(q64, k64, m64, c.table, c.page, past, T, scale)
+    qk = np.abs(q64).max() * np.abs(k64).sum(-1).max()
+    check(out, ref, A, m64.max(), qk, np.abs(q64).max(), max(lens), c.d, scale, c.dtype,
+          2.0 ** -11 if c.u4 else half_step(c.dtype), c.u4, what)
+    for b, n in enumerate(lens):  # rows that see nothing are zeros
+        for t in range(T):
+            if n - T + t < 0:
+                assert (out[b * T + t] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,u4,page,nk,G,d,T,lens", ATTN)
+def test_paged_attention(dtype, u4, page, nk, G, d, T, lens):
+    c = Pages(lens, page, nk, d, dtype, u4, 21)
+    q = strided(len(lens) * T, nk * G, d, dtype, 8).copy_(randn((len(lens) * T, nk * G, d), gen(6), dtype))
+    out, ws = run_attention(c, q, lens, T)
+    status_ok(ws)
+    check_attention(c, q, out, lens, T, d ** -0.5)
+    again, _ = run_attention(c, q, lens, T, ws=ws)   # the workspace serves again, the bits are the same
+    assert torch.equal(out, again)
+    status_ok(ws)
+
+
+@pytest.mark.parametrize("u4", [False, True])
+def test_paged_attention_large_scores_and_values(u4):
+    """Scores far apart (the running maximum moves), values far from 1."""
+    lens, T = [513, 40], 2
+    c = Pages(lens, 16, 2, 128, F16, u4, 33)
+    if u4:
+        c.v_scale.mul_(2.0 ** -9)
+        c.v_scale[..., 1] -= 0.5
+        c.k_scale.mul_(2)
+    else:
+        c.k.mul_(4)
+        c.v.mul_(1000)
+    q = randn((len(lens) * T, 8, 128), gen(8), F16) * 3
+    out, ws = run_attention(c, q, lens, T, scale=0.2)
+    status_ok(ws)
+    check_attention(c, q, out, lens, T, 0.2)
+
+
+def test_paged_attention_flags_bad_pages_and_skips_them():
+    lens, T, page = [100, 70], 1, 16
+    c = Pages(lens, page, 1, 64, F16, False, 41)
+    q = randn((2, 2, 64), gen(1), F16)
+    good, ws = run_attention(c, q, lens, T)
+    status_ok(ws)
+    c.t[0, 2] = c.k.shape[0] + 5
+    out, ws = run_attention(c, q, lens, T)
+    code, flags = ds.ds_workspace_status(ws)
+    assert flags == ds.DS_DEVFLAG_BAD_PAGE
+    assert torch.equal(out[1], good[1]) and torch.isfinite(out[0]).all()
+    c.t.copy_(i32(c.table))
+    out, ws = run_attention(c, q, [c.table.shape[1] * page + 1, 70], T)   # past the table
+    code, flags = ds.ds_workspace_status(ws)
+    assert flags & ds.DS_DEVFLAG_CACHE_OVERFLOW
+    assert torch.equal(out[1], good[1])
+    out, ws = run_attention(c, q, lens, T)
+    status_ok(ws)
+    assert torch.equal(out, good)
+
+
+def test_other_streams_graphs_and_shared_pages():
+    """Two calls at once on two streams (a workspace each), a captured and
+    replayed one with other lengths, and sequences that share their first pages."""
+    lens, T = [300, 77, 515], 1
+    c = Pages(lens, 16, 2, 128, BF16, True, 51)
+    c.t[1, :4] = c.t[0, :4]
+    c.table[1, :4] = c.table[0, :4]
+    q = randn((3, 8, 128), gen(3), BF16)
+    ref, _ = run_attention(c, q, lens, T)
+    torch.cuda.synchronize()
+    check_attention(c, q, ref, lens, T, 128 ** -0.5)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(run_attention(c, q, lens, T)[0])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], ref) and torch.equal(outs[1], ref)
+    past = i32([n - 1 for n in lens])
+    nb = ds.ds_paged_attention_workspace_bytes(c.handle, 8, 3, 1)
+    ws, out = new_workspace(nb), torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        ds.ds_paged_attention(c.handle, q, out, past, 3, 1, ws, nb)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
+    lens2 = [17, 76, 300]
+    past.copy_(i32([n - 1 for n in lens2]))
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    check_attention(c, q, out, lens2, T, 128 ** -0.5)
+    status_ok(ws)
+
+
+# ---------------------------------------------------------------- prompts
+PROMPTS = [
+    # dtype, heads, kv heads, d, query lengths, key lengths
+    (F16, 1, 1, 64, [1], [1]),
+    (F16, 4, 4, 64, [73, 29, 130, 0, 51, 1], None),
+    (BF16, 4, 1, 128, [127, 128, 129, 255, 256, 257], None),
+    (F16, 6, 2, 128, [600], None),
+    (BF16, 3, 3, 64, [1025, 3], None),
+    (F16, 2, 1, 128, [5, 130, 64, 0, 3], [300, 130, 1000, 9, 3]),
+    (BF16, 5, 5, 128, [17, 300], [18, 299]),          # the second: more queries than keys
+    (BF16, 8, 1, 64, [40, 7, 140], [0, 2, 513]),      # no keys at all
+    (F16, 16, 4, 128, [384], [2000]),
+]
+
+
+def run_prompt(q, k, v, cu_q, cu_k, B, out=None, scale=None, stream=None, ws=None):
+    nb = ds.ds_prompt_attention_workspace_bytes(q.shape[1], B, q.shape[0])
+    assert nb >= 256
+    ws = new_workspace(nb) if ws is None else ws
+    out = strided(q.shape[0], q.shape[1], q.shape[2], q.dtype, 8) if out is None else out
+    ds.ds_prompt_attention(q, k, v, out, cu_q, cu_k, B, ws, nb, scale, stream)
+    return out, ws
+
+
+def check_prompt(q, k, v, out, cu_q, cu_k, scale, what=""):
+    n = int(cu_q[-1])
+    q64, k64, v64 = to64(q), to64(k), to64(v)
+    ref, A = op.prompt_attention(q64, k64, v64, cu_q, cu_k, scale)
+    d = q.shape[2]
+    nk = int(cu_k[-1])
+    k_sum = np.abs(k64[:nk]).sum(-1).max() if nk else 0.0
+    qm = np.abs(q64[:n]).max()
+    longest = int(np.diff(cu_k).max())
+    check(out[:n], ref[:n], A[:n], np.abs(v64[:nk]).max() if nk else 0.0, qm * k_sum, qm, longest, d, scale, q.dtype,
+          half_step(q.dtype), what=what)
+
+
+@pytest.mark.parametrize("dtype,nh,nk,d,lq,lk", PROMPTS)
+def test_prompt_attention(dtype, nh, nk, d, lq, lk):
+    lk = lq if lk is None else lk
+    cu_q, cu_k = starts(lq), starts(lk)
+    pad = 5  # rows behind the last sequence: NaN, neither read into a result nor written
+    g = gen(13)
+    q, k, v = (strided(int(n) + pad, h, d, dtype, e) for n, h, e in ((cu_q[-1], nh, 8), (cu_k[-1], nk, 40), (cu_k[-1], nk, 16)))
+    for x, n in ((q, int(cu_q[-1])), (k, int(cu_k[-1])), (v, int(cu_k[-1]))):
+        x.fill_(float("nan"))
+        x[:n] = randn((n, x.shape[1], d), g, dtype)
+    out, ws = run_prompt(q, k, v, i32(cu_q), i32(cu_k), len(lq))
+    status_ok(ws)
+    check_prompt(q, k, v, out, cu_q, cu_k, d ** -0.5)
+    assert torch.isnan(out[int(cu_q[-1]):]).all()
+    for b in range(len(lq)):
+        blind = max(0, min(lq[b], lq[b] - lk[b]))
+        assert (out[int(cu_q[b]):int(cu_q[b]) + blind] == 0).all()
+    again, _ = run_prompt(q, k, v, i32(cu_q), i32(cu_k), len(lq), ws=ws)
+    n = int(cu_q[-1])
+    assert torch.equal(out[:n], again[:n])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_prompt_sequences_do_not_meet(dtype):
+    """Values that are not finite stay in their own sequence, at every place of a tile."""
+    lens = [100, 60, 140, 33]
+    cu = starts(lens)
+    g = gen(17)
+    q, k, v = (randn((int(cu[-1]), h, 128), g, dtype) for h in (4, 2, 2))
+    ref, _ = run_prompt(q, k, v, i32(cu), i32(cu), 4)
+    k2, v2 = k.clone(), v.clone()
+    k2[int(cu[1]):int(cu[2])] = float("inf")
+    v2[int(cu[1]):int(cu[2])] = float("nan")
+    out, _ = run_prompt(q, k2, v2, i32(cu), i32(cu), 4)
+    for b in (0, 2, 3):
+        assert torch.equal(out[int(cu[b]):int(cu[b + 1])], ref[int(cu[b]):int(cu[b + 1])]), b
+
+
+def test_prompt_scores_far_apart():
+    """The largest score comes late, in a later key tile, again and again; weights near and far from 1."""
+    n, d = 700, 128
+    g = gen(19)
+    q, k, v = randn((n, 2, d), g, F16), randn((n, 2, d), g, F16), randn((n, 2, d), g, F16) * 100
+    k.mul_(torch.linspace(0.2, 6, n, device="cuda")[:, None, None])
+    cu = starts([n])
+    out, ws = run_prompt(q, k, v, i32(cu), i32(cu), 1, scale=0.3)
+    status_ok(ws)
+    check_prompt(q, k, v, out, cu, cu, 0.3)
+
+
+def test_prompt_in_parts_of_one_projection_on_a_captured_stream():
+    lens = [200, 90]
+    cu = starts(lens)
+    n, nh, nk, d = int(cu[-1]), 6, 2, 64
+    qkv = randn((n, nh + 2 * nk, d), gen(23), BF16)
+    q, k, v = qkv[:, :nh], qkv[:, nh:nh + nk], qkv[:, nh + nk:]
+    t = i32(cu)
+    out = torch.empty(n, nh, d, dtype=BF16, device="cuda")
+    nb = ds.ds_prompt_attention_workspace_bytes(nh, 2, n)
+    ws = new_workspace(nb)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        ds.ds_prompt_attention(q, k, v, out, t, t, 2, ws, nb)
+    for lens in ([200, 90], [3, 280], [290, 0]):
+        cu = starts(lens)
+        t.copy_(i32(cu))
+        qkv.copy_(randn(qkv.shape, gen(sum(lens) + lens[0]), BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_prompt(q, k, v, out, cu, cu, d ** -0.5, str(lens))
+    status_ok(ws)
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("dtype,u4", [(F16, False), (BF16, False), (F16, True), (BF16, True)])
+def test_prompts_then_chunks_then_single_tokens(dtype, u4):
+    """Prompts enter the cache, a chunk attends gathered rows, then single tokens
+    are decoded: each output equals the oracle's over the rows the cache holds."""
+    page, nk, G, d, r = 16, 2, 4, 128, 128
+    nh, B = nk * G, 3
+    first, chunk, steps = [40, 1, 97], [20, 33, 5], 3
+    cap = [a + b + steps for a, b in zip(first, chunk)]
+    c = Pages(cap, page, nk, d, dtype, u4, 61)
+    tab = table_of(256, r)
+    rot = ds.rotary(tab)
+    ws = new_workspace(max(ds.ds_paged_attention_workspace_bytes(c.handle, nh, B, 1), ds.ds_prompt_attention_workspace_bytes(nh, B, 256)))
+    nb, g, scale = ws.numel(), gen(29), d ** -0.5
+    past = np.zeros(B, np.int64)
+    for new in (first, chunk):
+        cu, n = starts(new), sum(new)
+        q, k, v = (randn((n, h, d), g, dtype) for h in (nh, nk, nk))
+        qr = torch.empty_like(q)
+        ds.ds_paged_append(c.handle, q, k, v, qr, i32(cu), i32(past), B, rot, ws)
+        total = past + np.array(new)
+        cu_k = starts(total)
+        kg, vg = (torch.empty(int(cu_k[-1]), nk, d, dtype=dtype, device="cuda") for _ in range(2))
+        ds.ds_paged_gather(c.handle, kg, vg, i32(cu_k), i32(np.zeros(B)), B, ws)
+        out = torch.empty_like(q)
+        ds.ds_prompt_attention(qr, kg, vg, out, i32(cu), i32(cu_k), B, ws, nb)
+        torch.cuda.synchronize()
+        check_prompt(qr, kg, vg, out, cu, cu_k, scale, f"chunk {new}")
+        past = total
+    past_t = i32(past)
+    for step in range(steps):
+        q, k, v = (randn((B, h, d), g, dtype) for h in (nh, nk, nk))
+        qr, out = torch.empty_like(q), torch.empty_like(q)
+        ds.ds_paged_append(c.handle, q, k, v, qr, i32(np.arange(B + 1)), past_t, B, rot, ws)
+        ds.ds_paged_attention(c.handle, qr, out, past_t, B, 1, ws, nb)
+        torch.cuda.synchronize()
+        check_attention(c, qr, out, [int(p) + 1 for p in past], 1, scale, f"step {step}")
+        past = past + 1
+        past_t.add_(1)
+    status_ok(ws)
+
+
+def test_calls_off_the_device_are_refused():
+    c = Pages([20], 16, 1, 64, F16, False, 71)
+    q = randn((1, 1, 64), gen(1), F16)
+    ws = new_workspace(1 << 20)
+    n0 = ds.ds_launch_count()
+    host = torch.zeros(1, 1, 64, dtype=F16)
+    past, cu = i32([3]), i32([0, 1])
+    for call in (lambda: ds.ds_paged_attention(c.handle, host, torch.empty_like(q), past, 1, 1, ws, ws.numel()),
+                 lambda: ds.ds_paged_attention(c.handle, q, torch.empty_like(q), past.cpu(), 1, 1, ws, ws.numel()),
+                 lambda: ds.ds_paged_append(c.handle, None, host, q, None, cu, past, 1, None, ws),
+                 lambda: ds.ds_paged_gather(c.handle, host, q, cu, past, 1, ws),
+                 lambda: ds.ds_prompt_attention(q, host, q, torch.empty_like(q), cu, cu, 1, ws, ws.numel())):
+        with pytest.raises(ds.DSError) as e:
+            call()
+        assert e.value.code == ds.DS_ERR_INVALID_ARG
+    with pytest.raises(ds.DSError) as e:
+        ds.ds_paged_attention(c.handle, q, torch.empty_like(q), past, 1, 1, ws, 0)
+    assert e.value.code == ds.DS_ERR_WORKSPACE
+    assert ds.ds_launch_count() == n0

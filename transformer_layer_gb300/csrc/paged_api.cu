@@ -1,0 +1,338 @@
+// C entry points of the paged-cache operators (declared and documented in
+// ds_layer.h): argument checks before any launch, then the launches of
+// paged_append.cu, paged_attention.cu and prompt_attention.cu.
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <cstdio>
+
+#include "ds_layer.h"
+#include "internal.h"
+#include "paged.h"
+
+namespace ds {
+namespace {
+
+ds_status fail(ds_status s, const char* msg) {
+  set_last_error(msg);
+  return s;
+}
+ds_status launched(cudaError_t e, const char* what, int kernels) {
+  if (e != cudaSuccess) {
+    char msg[256];
+    snprintf(msg, sizeof(msg), "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+    return fail(DS_ERR_CUDA, msg);
+  }
+  add_launches(kernels);
+  return DS_OK;
+}
+
+bool multiple_of(const void* p, size_t n) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// SMs of the current device (0 on failure), looked up once per device.
+int device_sms(int* dev_out) {
+  static std::atomic<int> cache[64];
+  int dev = -1, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  *dev_out = dev;
+  sms = cache[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return 0;
+    }
+    cache[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
+}
+
+// A pointer that is not memory of the current device would fault in the
+// kernel, and a fault costs the caller the whole context: refuse it here.
+bool on_device(const void* p, int dev) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+}
+
+const char* kNotDevice = "a pointer is not memory of the current device";
+
+ds_status check_cache(const ds_paged_cache* c) {
+  if (c == nullptr) return fail(DS_ERR_INVALID_ARG, "cache is null");
+  if (c->act_dtype != DS_F16 && c->act_dtype != DS_BF16)
+    return fail(DS_ERR_INVALID_ARG, "act_dtype must be DS_F16 or DS_BF16");
+  if (c->dtype != c->act_dtype && c->dtype != DS_U4)
+    return fail(DS_ERR_UNSUPPORTED, "the pages hold act_dtype or DS_U4");
+  if (c->head_dim != 64 && c->head_dim != 128) return fail(DS_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(DS_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+  if (c->num_pages < 1 || c->table_stride < 1 || c->kv_heads < 1 || c->kv_heads > 65535)
+    return fail(DS_ERR_INVALID_ARG, "num_pages, table_stride and kv_heads must be positive (kv_heads up to 65535)");
+  if ((long long)c->table_stride * c->page_size > INT_MAX / 2)
+    return fail(DS_ERR_UNSUPPORTED, "table_stride * page_size must be below 2^30");
+  if (!multiple_of(c->k, 16) || !multiple_of(c->v, 16) || !multiple_of(c->block_table, 4))
+    return fail(DS_ERR_INVALID_ARG, "pages must be non-null and 16-byte aligned, block_table int32");
+  if (c->dtype == DS_U4 && (!multiple_of(c->k_scale, 16) || !multiple_of(c->v_scale, 16)))
+    return fail(DS_ERR_INVALID_ARG, "4-bit pages need k_scale and v_scale, 16-byte aligned");
+  return DS_OK;
+}
+
+ds_status check_cache_device(const ds_paged_cache* c, int dev) {
+  if (!on_device(c->k, dev) || !on_device(c->v, dev) || !on_device(c->block_table, dev) ||
+      (c->dtype == DS_U4 && (!on_device(c->k_scale, dev) || !on_device(c->v_scale, dev))))
+    return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  return DS_OK;
+}
+
+PagedView view(const ds_paged_cache* c) {
+  PagedView v;
+  v.k = c->k;
+  v.v = c->v;
+  v.k_scale = c->k_scale;
+  v.v_scale = c->v_scale;
+  v.table = c->block_table;
+  v.num_pages = c->num_pages;
+  v.page_shift = c->page_size == 16 ? 4 : (c->page_size == 32 ? 5 : (c->page_size == 64 ? 6 : 7));
+  v.table_stride = c->table_stride;
+  v.kv_heads = c->kv_heads;
+  v.head_dim = c->head_dim;
+  v.u4 = c->dtype == DS_U4;
+  v.act = c->act_dtype == DS_BF16 ? ActKind::BF16 : ActKind::F16;
+  return v;
+}
+
+// A packed tensor's pointer and token stride.
+ds_status check_packed(const void* p, int64_t stride, int heads, int head_dim) {
+  if (!multiple_of(p, 16)) return fail(DS_ERR_INVALID_ARG, "packed tensors must be non-null and 16-byte aligned");
+  if (stride % 8 != 0 || stride < (int64_t)heads * head_dim || stride > ((int64_t)1 << 31))
+    return fail(DS_ERR_INVALID_ARG, "a token stride must be a multiple of 8 elements, heads * head_dim to 2^31");
+  return DS_OK;
+}
+
+ds_status check_ws(const void* ws, size_t bytes, size_t need) {
+  if (!multiple_of(ws, 256)) return fail(DS_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  if (bytes < need) return fail(DS_ERR_WORKSPACE, "workspace too small");
+  return DS_OK;
+}
+
+ds_status check_batch(int tokens, int batch, const void* cu, const void* len) {
+  if (batch < 1 || batch > 65535) return fail(DS_ERR_INVALID_ARG, "batch must be in 1 .. 65535");
+  if (tokens < 0 || tokens > (1 << 24)) return fail(DS_ERR_INVALID_ARG, "tokens must be in 0 .. 2^24");
+  if (!multiple_of(cu, 4) || !multiple_of(len, 4))
+    return fail(DS_ERR_INVALID_ARG, "cu_seqlens and the positions must be non-null int32 device arrays");
+  return DS_OK;
+}
+
+float scale_log2(float scale) { return (float)((double)scale * 1.4426950408889634); }
+
+}  // namespace
+}  // namespace ds
+
+using namespace ds;
+
+#define DS_TRY(x)                     \
+  do {                                \
+    const ds_status s_ = (x);         \
+    if (s_ != DS_OK) return s_;       \
+  } while (0)
+
+extern "C" {
+
+ds_status ds_paged_append(const ds_paged_cache* cache, const ds_rotary* rotary, const void* q, void* q_out, int heads,
+                          const void* k, const void* v, int64_t q_stride, int64_t q_out_stride, int64_t k_stride,
+                          int64_t v_stride, int tokens, const int32_t* cu_seqlens, const int32_t* past_len, int batch,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  DS_TRY(check_cache(cache));
+  DS_TRY(check_batch(tokens, batch, cu_seqlens, past_len));
+  DS_TRY(check_ws(workspace, ws_bytes, 256));
+  if (tokens == 0) return DS_OK;
+  const int d = cache->head_dim;
+  DS_TRY(check_packed(k, k_stride, cache->kv_heads, d));
+  DS_TRY(check_packed(v, v_stride, cache->kv_heads, d));
+  if (q != nullptr) {
+    if (heads < 1 || heads > 65535) return fail(DS_ERR_INVALID_ARG, "heads must be in 1 .. 65535");
+    DS_TRY(check_packed(q, q_stride, heads, d));
+    DS_TRY(check_packed(q_out, q_out_stride, heads, d));
+    if (q == q_out && q_stride != q_out_stride)
+      return fail(DS_ERR_INVALID_ARG, "q rotated in place needs one stride");
+  }
+  if (rotary != nullptr) {
+    if (!multiple_of(rotary->cos_sin, 16) || rotary->max_pos < 1)
+      return fail(DS_ERR_INVALID_ARG, "the rotation table must be non-null, 16-byte aligned, with max_pos >= 1");
+    if (rotary->rotary_dim < 16 || rotary->rotary_dim > d || rotary->rotary_dim % 16 != 0)
+      return fail(DS_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 up to head_dim");
+    if (rotary->interleaved != 0 && rotary->interleaved != 1)
+      return fail(DS_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  }
+  int dev = -1;
+  const int sms = device_sms(&dev);
+  if (sms == 0) return fail(DS_ERR_CUDA, "no CUDA device");
+  DS_TRY(check_cache_device(cache, dev));
+  if (!on_device(k, dev) || !on_device(v, dev) || !on_device(cu_seqlens, dev) || !on_device(past_len, dev) ||
+      !on_device(workspace, dev) || (q != nullptr && (!on_device(q, dev) || !on_device(q_out, dev))) ||
+      (rotary != nullptr && !on_device(rotary->cos_sin, dev)))
+    return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  PagedAppendArgs a;
+  a.c = view(cache);
+  if (rotary != nullptr) {
+    a.cos_sin = rotary->cos_sin;
+    a.max_pos = rotary->max_pos;
+    a.rotary_dim = rotary->rotary_dim;
+    a.interleaved = rotary->interleaved;
+  }
+  a.q = q;
+  a.q_out = q_out;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.heads = heads;
+  a.tokens = tokens;
+  a.batch = batch;
+  a.cu = cu_seqlens;
+  a.past = past_len;
+  a.status = static_cast<unsigned*>(workspace);
+  return launched(launch_paged_append(a, sms, static_cast<cudaStream_t>(stream)), "paged append launch", 1);
+}
+
+ds_status ds_paged_gather(const ds_paged_cache* cache, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                          int tokens, const int32_t* cu_seqlens, const int32_t* first_pos, int batch, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  DS_TRY(check_cache(cache));
+  DS_TRY(check_batch(tokens, batch, cu_seqlens, first_pos));
+  DS_TRY(check_ws(workspace, ws_bytes, 256));
+  if (tokens == 0) return DS_OK;
+  DS_TRY(check_packed(k_out, k_stride, cache->kv_heads, cache->head_dim));
+  DS_TRY(check_packed(v_out, v_stride, cache->kv_heads, cache->head_dim));
+  int dev = -1;
+  const int sms = device_sms(&dev);
+  if (sms == 0) return fail(DS_ERR_CUDA, "no CUDA device");
+  DS_TRY(check_cache_device(cache, dev));
+  if (!on_device(k_out, dev) || !on_device(v_out, dev) || !on_device(cu_seqlens, dev) || !on_device(first_pos, dev) ||
+      !on_device(workspace, dev))
+    return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  PagedGatherArgs a;
+  a.c = view(cache);
+  a.k = k_out;
+  a.v = v_out;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.tokens = tokens;
+  a.batch = batch;
+  a.cu = cu_seqlens;
+  a.first = first_pos;
+  a.status = static_cast<unsigned*>(workspace);
+  return launched(launch_paged_gather(a, sms, static_cast<cudaStream_t>(stream)), "paged gather launch", 1);
+}
+
+size_t ds_paged_attention_workspace_bytes(const ds_paged_cache* cache, int heads, int batch, int new_tokens) {
+  if (check_cache(cache) != DS_OK) return 0;
+  if (heads < 1 || heads > 65535 || heads % cache->kv_heads != 0 || batch < 1 || batch > 65535 || new_tokens < 1 ||
+      new_tokens > 16)
+    return 0;
+  int dev = -1;
+  const int sms = device_sms(&dev);
+  return sms == 0 ? 0 : paged_attention_ws_bytes(view(cache), heads, batch, new_tokens, sms);
+}
+
+ds_status ds_paged_attention(const ds_paged_cache* cache, const void* q, void* out, int heads, int64_t q_stride,
+                             int64_t out_stride, const int32_t* past_len, int batch, int new_tokens, float scale,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  DS_TRY(check_cache(cache));
+  if (heads < 1 || heads > 65535 || heads % cache->kv_heads != 0)
+    return fail(DS_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads, up to 65535");
+  if (batch < 1 || batch > 65535) return fail(DS_ERR_INVALID_ARG, "batch must be in 1 .. 65535");
+  if (new_tokens < 1 || new_tokens > 16) return fail(DS_ERR_UNSUPPORTED, "new_tokens must be in 1 .. 16");
+  if (!std::isfinite(scale)) return fail(DS_ERR_INVALID_ARG, "scale must be finite");
+  DS_TRY(check_packed(q, q_stride, heads, cache->head_dim));
+  DS_TRY(check_packed(out, out_stride, heads, cache->head_dim));
+  if (q == out) return fail(DS_ERR_INVALID_ARG, "out must not alias q");
+  if (!multiple_of(past_len, 4)) return fail(DS_ERR_INVALID_ARG, "past_len must be a non-null int32 device array");
+  int dev = -1;
+  const int sms = device_sms(&dev);
+  if (sms == 0) return fail(DS_ERR_CUDA, "no CUDA device");
+  PagedAttnArgs a;
+  a.c = view(cache);
+  DS_TRY(check_ws(workspace, ws_bytes, paged_attention_ws_bytes(a.c, heads, batch, new_tokens, sms)));
+  DS_TRY(check_cache_device(cache, dev));
+  if (!on_device(q, dev) || !on_device(out, dev) || !on_device(past_len, dev) || !on_device(workspace, dev))
+    return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.heads = heads;
+  a.batch = batch;
+  a.T = new_tokens;
+  a.past = past_len;
+  a.scale_log2 = scale_log2(scale);
+  a.status = static_cast<unsigned*>(workspace);
+  return launched(launch_paged_attention(a, workspace, sms, static_cast<cudaStream_t>(stream)),
+                  "paged attention launch", 1);
+}
+
+size_t ds_prompt_attention_workspace_bytes(int heads, int batch, int tokens) {
+  if (heads < 1 || heads > 65535 || batch < 1 || batch > 65535 || tokens < 0 || tokens > (1 << 24)) return 0;
+  return prompt_attention_ws_bytes(heads, batch, tokens);
+}
+
+ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void* out, int heads, int kv_heads,
+                              int head_dim, ds_dtype act_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              int64_t out_stride, int q_tokens, int k_tokens, const int32_t* cu_q,
+                              const int32_t* cu_k, int batch, float scale, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  if (act_dtype != DS_F16 && act_dtype != DS_BF16)
+    return fail(DS_ERR_INVALID_ARG, "act_dtype must be DS_F16 or DS_BF16");
+  if (head_dim != 64 && head_dim != 128) return fail(DS_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (kv_heads < 1 || heads < 1 || heads > 65535 || heads % kv_heads != 0)
+    return fail(DS_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads, up to 65535");
+  DS_TRY(check_batch(q_tokens, batch, cu_q, cu_k));
+  if (k_tokens < 0 || k_tokens > (1 << 24)) return fail(DS_ERR_INVALID_ARG, "k_tokens must be in 0 .. 2^24");
+  if (!std::isfinite(scale)) return fail(DS_ERR_INVALID_ARG, "scale must be finite");
+  DS_TRY(check_ws(workspace, ws_bytes, prompt_attention_ws_bytes(heads, batch, q_tokens)));
+  if (q_tokens == 0) return DS_OK;
+  DS_TRY(check_packed(q, q_stride, heads, head_dim));
+  DS_TRY(check_packed(out, out_stride, heads, head_dim));
+  if (k_tokens > 0) {
+    DS_TRY(check_packed(k, k_stride, kv_heads, head_dim));
+    DS_TRY(check_packed(v, v_stride, kv_heads, head_dim));
+  }
+  if (out == q || out == k || out == v) return fail(DS_ERR_INVALID_ARG, "out must not alias an input");
+  int dev = -1;
+  const int sms = device_sms(&dev);
+  if (sms == 0) return fail(DS_ERR_CUDA, "no CUDA device");
+  if (!on_device(q, dev) || !on_device(out, dev) || !on_device(cu_q, dev) || !on_device(cu_k, dev) ||
+      !on_device(workspace, dev) || (k_tokens > 0 && (!on_device(k, dev) || !on_device(v, dev))))
+    return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  PromptAttnArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.act = act_dtype == DS_BF16 ? ActKind::BF16 : ActKind::F16;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out_stride = out_stride;
+  a.q_tokens = q_tokens;
+  a.k_tokens = k_tokens;
+  a.batch = batch;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.scale_log2 = scale_log2(scale);
+  a.status = static_cast<unsigned*>(workspace);
+  return launched(launch_prompt_attention(a, workspace, sms, static_cast<cudaStream_t>(stream)),
+                  "prompt attention launch", 1);
+}
+
+}  // extern "C"

@@ -16,10 +16,11 @@ LIB_PATH = os.path.join(_PKG, "libdslayer.so")
 LIB_DEBUG_BOUNDS_PATH = os.path.join(_PKG, "libdslayer_debug_bounds.so")  # diagnostic build
 
 DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED, DS_ERR_CUDA, DS_ERR_WORKSPACE, DS_ERR_DEVICE = range(6)
-DS_F16, DS_BF16, DS_I8 = 0, 1, 2
+DS_F16, DS_BF16, DS_I8, DS_U4 = 0, 1, 2, 3
 DS_DEVFLAG_CACHE_OVERFLOW = 0x1
 DS_DEVFLAG_WAIT_TIMEOUT = 0x2
 DS_DEVFLAG_BOUNDS = 0x4
+DS_DEVFLAG_BAD_PAGE = 0x8
 
 # Every exported symbol of include/ds_layer.h, with (restype, argtypes).
 _vp = C.c_void_p
@@ -60,6 +61,17 @@ _SIGS = {
                                           C.c_size_t, _vp]),
     "ds_tp_ffn_partial": (C.c_int, [_vp, _vp, _vp, C.c_int, _vp, C.c_size_t, _vp]),
     "ds_tp_finish": (C.c_int, [_vp, _vp, _vp, C.c_int, _vp]),
+    "ds_paged_append": (C.c_int, [_vp, _vp, _vp, _vp, C.c_int, _vp, _vp, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                  C.c_int, _vp, _vp, C.c_int, _vp, C.c_size_t, _vp]),
+    "ds_paged_gather": (C.c_int, [_vp, _vp, _vp, C.c_int64, C.c_int64, C.c_int, _vp, _vp, C.c_int, _vp, C.c_size_t,
+                                  _vp]),
+    "ds_paged_attention_workspace_bytes": (C.c_size_t, [_vp, C.c_int, C.c_int, C.c_int]),
+    "ds_paged_attention": (C.c_int, [_vp, _vp, _vp, C.c_int, C.c_int64, C.c_int64, _vp, C.c_int, C.c_int, C.c_float,
+                                     _vp, C.c_size_t, _vp]),
+    "ds_prompt_attention_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
+    "ds_prompt_attention": (C.c_int, [_vp, _vp, _vp, _vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int64, C.c_int64,
+                                      C.c_int64, C.c_int64, C.c_int, C.c_int, _vp, _vp, C.c_int, C.c_float, _vp,
+                                      C.c_size_t, _vp]),
     "ds_launch_count": (C.c_uint64, []),
     "ds_status_string": (C.c_char_p, [C.c_int]),
     "ds_last_error": (C.c_char_p, []),
@@ -104,6 +116,16 @@ TP_MATRIX_NAMES = ("w_qkv", "b_qkv", "w_o", "w_fc1", "b_fc1", "w_fc2")
 
 class ds_tp_block(C.Structure):
     _fields_ = [(n, C.c_int) for n in ("matrix", "src_row", "src_col", "rows", "cols", "src_cols", "dst_row")]
+
+
+class ds_paged_cache(C.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp),
+                ("num_pages", C.c_int), ("page_size", C.c_int), ("table_stride", C.c_int), ("kv_heads", C.c_int),
+                ("head_dim", C.c_int), ("dtype", C.c_int), ("act_dtype", C.c_int)]
+
+
+class ds_rotary(C.Structure):
+    _fields_ = [("cos_sin", _vp), ("max_pos", C.c_int), ("rotary_dim", C.c_int), ("interleaved", C.c_int)]
 
 
 class DSError(RuntimeError):
@@ -381,6 +403,139 @@ def tp_layer_forward(layer, x_in, x_out, batch, new_tokens, k_cache, v_cache, ma
     ds_tp_ffn_partial(layer, x1, y, rows, ws, ws_bytes)
     dist.all_reduce(y, op=dist.ReduceOp.SUM, group=group)
     ds_tp_finish(layer, y, x_out, rows)
+
+
+# ---------------------------------------------------------------- paged cache
+def _check_like(t, shape, dtype, what):
+    """A tensor of this shape (None: any) and dtype, contiguous."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)) \
+            or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())}")
+
+
+def _check_int32(t, numel, what):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < numel or (numel > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what}: expected an int32 vector of at least {numel} elements, got {t.dtype} {tuple(t.shape)}")
+
+
+def _packed(t, dtype, heads, head_dim, what):
+    """Token stride in elements of a packed tensor [tokens][heads][head_dim]."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads) or \
+            t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{what}: expected a {dtype} tensor [tokens][{heads if heads is not None else 'heads'}]"
+                         f"[{head_dim}] with contiguous heads, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim
+
+
+def paged_cache(k, v, block_table, act_dtype, k_scale=None, v_scale=None):
+    """The ds_paged_cache of pages k, v [num_pages][kv_heads][page_size][head_dim]
+    (act_dtype), or [...][head_dim / 2] uint8 codes with k_scale, v_scale
+    [num_pages][kv_heads][page_size][2] float16, and a block table
+    [batch][pages per sequence] int32.  The struct keeps the tensors alive."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("k: expected pages [num_pages][kv_heads][page_size][head_dim]")
+    codes = k.dtype == torch.uint8
+    if codes and (k_scale is None or v_scale is None):
+        raise ValueError("4-bit pages need k_scale and v_scale")
+    num_pages, kv_heads, page_size, row = k.shape
+    for t, what in ((k, "k"), (v, "v")):
+        _check_like(t, k.shape, torch.uint8 if codes else act_dtype, what)
+    if codes:
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _check_like(t, (num_pages, kv_heads, page_size, 2), torch.float16, what)
+    _check_like(block_table, (None, None), torch.int32, "block_table")
+    c = ds_paged_cache(_ptr(k), _ptr(v), _ptr(k_scale) if codes else None, _ptr(v_scale) if codes else None,
+                       _ptr(block_table), num_pages, page_size, block_table.shape[1], kv_heads,
+                       2 * row if codes else row, DS_U4 if codes else _dtype_code(act_dtype), _dtype_code(act_dtype))
+    c.tensors = (k, v, k_scale, v_scale, block_table)
+    c.torch_dtype = act_dtype
+    return c
+
+
+def rotary(cos_sin, interleaved=False):
+    """The ds_rotary of a float32 table [max_pos][rotary_dim] (cosines, then
+    sines, of each position's angles).  The struct keeps the table alive."""
+    import torch
+    _check_like(cos_sin, (None, None), torch.float32, "cos_sin")
+    r = ds_rotary(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
+    r.tensors = (cos_sin,)
+    return r
+
+
+def _check_batch(cache, batch):
+    if cache.tensors[4].shape[0] < batch:
+        raise ValueError(f"block_table: {cache.tensors[4].shape[0]} rows for a batch of {batch}")
+
+
+def ds_paged_append(cache, q, k, v, q_out, cu_seqlens, past_len, batch, rotary, ws, stream=None):
+    """q (and q_out) and rotary may be None; a workspace tensor of 256 bytes or more."""
+    tokens, nk, d, dt = k.shape[0], cache.kv_heads, cache.head_dim, cache.torch_dtype
+    ks, vs = _packed(k, dt, nk, d, "k"), _packed(v, dt, nk, d, "v")
+    heads = qs = qos = 0
+    if q is not None:
+        heads = q.shape[1]
+        qs, qos = _packed(q, dt, heads, d, "q"), _packed(q_out, dt, heads, d, "q_out")
+    if v.shape[0] != tokens or (q is not None and not q.shape[0] == q_out.shape[0] == tokens):
+        raise ValueError("q, k, v and q_out must have the same number of tokens")
+    _check_int32(cu_seqlens, batch + 1, "cu_seqlens")
+    _check_int32(past_len, batch, "past_len")
+    _check_batch(cache, batch)
+    _check(load().ds_paged_append(C.byref(cache), C.byref(rotary) if rotary is not None else None, _ptr(q),
+                                  _ptr(q_out) if q is not None else None, heads, _ptr(k), _ptr(v), qs, qos, ks, vs,
+                                  tokens, _ptr(cu_seqlens), _ptr(past_len), batch, _ptr(ws), ws.numel(),
+                                  _stream(stream)), "ds_paged_append")
+
+
+def ds_paged_gather(cache, k_out, v_out, cu_seqlens, first_pos, batch, ws, stream=None):
+    tokens, nk, d, dt = k_out.shape[0], cache.kv_heads, cache.head_dim, cache.torch_dtype
+    ks, vs = _packed(k_out, dt, nk, d, "k_out"), _packed(v_out, dt, nk, d, "v_out")
+    if v_out.shape[0] != tokens:
+        raise ValueError("k_out and v_out must have the same number of tokens")
+    _check_int32(cu_seqlens, batch + 1, "cu_seqlens")
+    _check_int32(first_pos, batch, "first_pos")
+    _check_batch(cache, batch)
+    _check(load().ds_paged_gather(C.byref(cache), _ptr(k_out), _ptr(v_out), ks, vs, tokens, _ptr(cu_seqlens),
+                                  _ptr(first_pos), batch, _ptr(ws), ws.numel(), _stream(stream)), "ds_paged_gather")
+
+
+def ds_paged_attention_workspace_bytes(cache, heads, batch, new_tokens):
+    return int(load().ds_paged_attention_workspace_bytes(C.byref(cache), heads, batch, new_tokens))
+
+
+def ds_paged_attention(cache, q, out, past_len, batch, new_tokens, ws, ws_bytes, scale=None, stream=None):
+    """scale None: 1 / sqrt(head_dim)."""
+    heads, d, dt = q.shape[1], cache.head_dim, cache.torch_dtype
+    qs, os_ = _packed(q, dt, heads, d, "q"), _packed(out, dt, heads, d, "out")
+    if q.shape[0] != batch * new_tokens or out.shape[0] != q.shape[0]:
+        raise ValueError("q and out must have batch * new_tokens rows")
+    _check_int32(past_len, batch, "past_len")
+    _check_batch(cache, batch)
+    _check(load().ds_paged_attention(C.byref(cache), _ptr(q), _ptr(out), heads, qs, os_, _ptr(past_len), batch,
+                                     new_tokens, scale if scale is not None else d ** -0.5, _ptr(ws), ws_bytes,
+                                     _stream(stream)), "ds_paged_attention")
+
+
+def ds_prompt_attention_workspace_bytes(heads, batch, tokens):
+    return int(load().ds_prompt_attention_workspace_bytes(heads, batch, tokens))
+
+
+def ds_prompt_attention(q, k, v, out, cu_q, cu_k, batch, ws, ws_bytes, scale=None, stream=None):
+    """q, out [q_tokens][heads][head_dim]; k, v [k_tokens][kv_heads][head_dim];
+    scale None: 1 / sqrt(head_dim)."""
+    dt, (nq, heads, d), (nk, kv_heads, _) = q.dtype, q.shape, k.shape
+    qs, ks = _packed(q, dt, heads, d, "q"), _packed(k, dt, kv_heads, d, "k")
+    vs, os_ = _packed(v, dt, kv_heads, d, "v"), _packed(out, dt, heads, d, "out")
+    if out.shape[0] != nq or v.shape[0] != nk:
+        raise ValueError("q and out, and k and v, must have the same number of tokens")
+    _check_int32(cu_q, batch + 1, "cu_q")
+    _check_int32(cu_k, batch + 1, "cu_k")
+    _check(load().ds_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(out), heads, kv_heads, d, _dtype_code(dt), qs,
+                                      ks, vs, os_, nq, nk, _ptr(cu_q), _ptr(cu_k), batch,
+                                      scale if scale is not None else d ** -0.5, _ptr(ws), ws_bytes,
+                                      _stream(stream)), "ds_prompt_attention")
 
 
 def ds_launch_count():
