@@ -344,7 +344,8 @@ def test_paged_attention_flags_bad_pages_and_skips_them():
     out, ws = run_attention(c, q, [c.table.shape[1] * page + 1, 70], T)   # past the table
     code, flags = ds.ds_workspace_status(ws)
     assert flags & ds.DS_DEVFLAG_CACHE_OVERFLOW
-    assert torch.equal(out[1], good[1])
+    # (the other lengths of a batch may move the places at which a row's sum is split)
+    assert (out[1].float() - good[1].float()).abs().max() <= 4 * 2.0 ** -11 * np.nanmax(to64(c.v))
     out, ws = run_attention(c, q, lens, T)
     status_ok(ws)
     assert torch.equal(out, good)

@@ -1,112 +1,748 @@
 // Attention of a few new tokens per sequence over a paged cache
 // (ds_paged_attention), pages in 16 bits or in 4.
 //
-// Mathematics, per (sequence b, new token t, head h): s_j = scale q . k_j for
-// positions j <= past[b] + t, p = softmax(s), out = sum_j p_j v_j; a 4-bit row
-// stands for code * scale + minimum.  A row without positions is zeros.
+// Page cited: "DeepSpeed Inference 内核优化深度解析：多 GPU 自适应并行、算子融合推理内核
+// 与 MoQ 量化支持", §3.2 region 2 (attention over the cache, the head-split
+// layout read by index arithmetic); pages, grouped heads and 4-bit rows are
+// this library's own extension.
 //
-// First form: one CTA per (row, head), its warps take every 4th position with
-// a running maximum and sum each, and meet in shared memory.
+// Mathematics, per (sequence b, new token t, head h): s_j = scale q . k_j for
+// positions j <= past[b] + t, p = softmax(s), out = sum_j p_j v_j.  The G
+// query heads of a key head and the T tokens are rows r = t G + g of one
+// product, so a key or value row is read once for all of them.  A 4-bit row
+// stands for c s + m (codes c, scale s, minimum m):
+//   q . k = s (q . c) + m sum(q),   sum_j p_j v_j = sum_j (p_j s_j) c_j + sum_j p_j m_j,
+// so the products run on the codes and the scales act on one number per
+// (row, key).
+//
+// Bound: reading K and V once (HBM).  Per warp and 16 positions:
+//  * S^T = K Q^T by mma.sync m16n8k16, 16 positions x 8 rows: the keys are the
+//    16-row operand, so one fragment of K (or V) serves every 8 query rows, and
+//    up to 8 rows cost one product.  O^T = V^T P^T likewise; P^T comes from S^T
+//    by movmatrix.  tcgen05's smallest tile (M = 64 or 128 x N = 8) would need
+//    P written to shared or tensor memory and a barrier per step for products
+//    that use under a sixth of mma.sync's rate here.
+//  * codes become fp16 operands by one AND: a four-bit field at bit 0 or 4 of a
+//    16-bit half is the subnormal number c 2^-24 or c 2^-20, which the tensor
+//    cores multiply exactly; the powers of two go into the scales.
+//  * running maximum per row (log2 domain), sums per lane; O is only rescaled
+//    in the steps in which a maximum rises.
+// Copies: each warp streams its own tiles (16 to 64 positions) through a ring of
+// three or four stages with cp.async, 16-byte chunks XOR-swizzled; rows past the
+// sequence are zero-filled without being read.  A tile's 16-position blocks lie
+// in one page each.  No barrier between warps until the end of a segment.
+//
+// Split: a segment is (sequence, key head, group of 8 or 16 rows), its length
+// known on the device only.  Every CTA takes the same number of 16-position
+// blocks of the segments laid end to end (two CTAs per SM), whatever the
+// lengths; a segment that crosses CTAs leaves partial sums in the workspace,
+// and the last CTA to arrive joins them in order (the same bits every time).
+#include <math.h>
+
+#include <atomic>
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace ds {
 
-constexpr int kSimpleThreads = 128;
+constexpr int kPaWarps = 4;
+constexpr int kPaThreads = kPaWarps * 32;
+constexpr int kPaCtasPerSm = 2;
 
-template <typename ACT, int D, bool U4>
-__global__ void __launch_bounds__(kSimpleThreads) paged_attention_kernel(const PagedAttnArgs a) {
-  constexpr int C = D / 32;  // channels per lane
-  constexpr int W = kSimpleThreads / 32;
-  __shared__ float so[W][D], sm[W], sl[W];
-  const int row = blockIdx.x, h = blockIdx.y;
-  const int b = row / a.T, t = row % a.T;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kh = h / (a.heads / a.c.kv_heads);
-  const int n = a.past[b] + t + 1;
-  const ACT* q = static_cast<const ACT*>(a.q) + (size_t)row * a.q_stride + (size_t)h * D + lane * C;
-  float qv[C], o[C], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    qv[i] = Act<ACT>::to_f(q[i]) * a.scale_log2;
-    o[i] = 0.f;
-  }
-  unsigned bad = 0;
-  const long long cap = (long long)a.c.table_stride << a.c.page_shift;
-  if (n > cap) bad |= kFlagCacheOverflow;
-  for (int j = warp; j < n && j < cap; j += W) {
-    unsigned why = 0;
-    long long r = page_row(a.c, b, j, &why);
-    bad |= why;
-    if (r < 0) continue;
-    r += (long long)kh << a.c.page_shift;
-    float kv[C], vv[C];
-    if constexpr (U4) {
-      const float2 ks = __half22float2(static_cast<const __half2*>(a.c.k_scale)[r]);
-      const float2 vs = __half22float2(static_cast<const __half2*>(a.c.v_scale)[r]);
-#pragma unroll
-      for (int i = 0; i < C; i += 2) {
-        const size_t at = ((size_t)r * D + lane * C + i) / 2;
-        const unsigned kb = static_cast<const uint8_t*>(a.c.k)[at], vb = static_cast<const uint8_t*>(a.c.v)[at];
-        kv[i] = (kb & 15) * ks.x + ks.y;
-        kv[i + 1] = (kb >> 4) * ks.x + ks.y;
-        vv[i] = (vb & 15) * vs.x + vs.y;
-        vv[i + 1] = (vb >> 4) * vs.x + vs.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        kv[i] = Act<ACT>::to_f(static_cast<const ACT*>(a.c.k)[r * D + lane * C + i]);
-        vv[i] = Act<ACT>::to_f(static_cast<const ACT*>(a.c.v)[r * D + lane * C + i]);
-      }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) s += qv[i] * kv[i];
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * al + p;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = o[i] * al + p * vv[i];
-    m = mn;
-  }
-  if (bad != 0 && lane == 0) atomicOr(a.status, bad);
-#pragma unroll
-  for (int i = 0; i < C; ++i) so[warp][lane * C + i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY;
-    for (int w = 0; w < W; ++w) M = fmaxf(M, sm[w]);
-    float L = 0.f, O = 0.f;
-    for (int w = 0; w < W; ++w) {
-      const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - M);
-      L += f * sl[w];
-      O += f * so[w][threadIdx.x];
-    }
-    static_cast<ACT*>(a.out)[(size_t)row * a.out_stride + (size_t)h * D + threadIdx.x] =
-        Act<ACT>::from_f(L > 0.f ? O / L : 0.f);
-  }
+__device__ __forceinline__ void pa_cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void pa_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void pa_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void pa_ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void pa_ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void pa_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value) mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
+  else mma_bf16(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
-size_t paged_attention_ws_bytes(const PagedView&, int, int, int, int) { return 256; }
+// One warp tile: KB blocks of 16 positions.  A block's bytes in a stage: K rows,
+// V rows, and for 4-bit pages the (scale, minimum) pairs of K and V.
+template <int D, bool U4>
+struct PaTile {
+  static constexpr int KB = U4 ? 4 : (D == 128 ? 1 : 2);
+  static constexpr int ROW = U4 ? D / 2 : D * 2;  // bytes of a row
+  static constexpr int BLOCK = 2 * 16 * ROW + (U4 ? 128 : 0);
+  static constexpr int STAGE = KB * BLOCK;
+  static constexpr int NST = U4 && D == 64 ? 4 : 3;
+  static constexpr int SMEM = kPaWarps * NST * STAGE;
+  // Byte offset of 16-byte chunk c of row r among a block's rows: ldmatrix reads
+  // 8 rows at one chunk, the code loads 4 rows at 16 or 32 bytes.
+  static __device__ __forceinline__ uint32_t off(int r, int c) {
+    if constexpr (!U4) return (uint32_t)(r * ROW + ((c ^ (r & 7)) << 4));
+    else if constexpr (D == 128) return (uint32_t)(r * ROW + ((c ^ (r & 2)) << 4));
+    else return (uint32_t)(r * ROW + (c << 4));
+  }
+  // 4-bit: the position of the block that operand row i holds.  Rows 2c and 2c + 1
+  // pair up in the value product; the pairs are chosen so that the loads of four
+  // rows at once meet no bank twice.
+  static __device__ __forceinline__ int key(int i) {
+    const int c = (i >> 1) & 3;
+    return (i & 8) + ((i & 1) ? ((c + 4) ^ (D == 128 ? 1 : 2)) : c);
+  }
+};
+
+// Where a launch's blocks lie: segments (b, key head, row group) end to end,
+// sequence b having `per_b` segments of nb(b) blocks each.
+struct PaPlan {
+  int nrt = 1;          // row groups per (sequence, key head)
+  int min_chunk = 4;    // blocks a CTA takes at least
+  float* part_o = nullptr;   // [CTA][2][rows][D]
+  float* part_ml = nullptr;  // [CTA][2][rows][2]
+  int* counters = nullptr;   // [segments], zero between calls
+};
+
+__device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
+  const int cap = a.c.table_stride << a.c.page_shift;
+  return max(0, min(min(a.past[b], cap) + a.T, cap));
+}
+__device__ __forceinline__ int pa_blocks(const PagedAttnArgs& a, int b) { return max(1, (pa_len(a, b) + 15) >> 4); }
+
+template <typename ACT, int D, bool U4, int NR>
+__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
+    paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ PaPlan pl) {
+  using Tile = PaTile<D, U4>;
+  constexpr int KB = Tile::KB, NST = Tile::NST, ROW = Tile::ROW;
+  constexpr int RP = 8 * NR;    // rows of a segment
+  constexpr int MT = D / 16;    // 16-channel tiles of O^T
+  constexpr int KS = D / 16;    // 16-channel steps of S^T
+  constexpr int OS = D + 4;     // row stride of the merge buffer: conflict-free
+  using OP = typename std::conditional<U4, __half, ACT>::type;  // type of the products' operands
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ long long s_scan[kPaWarps];
+  __shared__ long long s_first[3];  // blocks before the start's sequence, its index, all blocks
+  __shared__ float s_m[kPaWarps][RP], s_l[kPaWarps][RP];
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
+  const int G = a.heads / a.c.kv_heads, R = G * a.T, B = a.batch;
+  const int per_b = a.c.kv_heads * pl.nrt;
+  const uint32_t stage0 = smem_u32(sm) + (uint32_t)(warp * NST * Tile::STAGE);
+
+  // ---- this CTA's share: blocks [c_lo, c_hi) of all segments' blocks
+  long long chunk, c_lo, c_hi;
+  {
+    const int per = (B + kPaThreads - 1) / kPaThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    long long sum = 0;
+    unsigned over = 0;
+    for (int b = b0; b < b1; ++b) {
+      sum += (long long)pa_blocks(a, b) * per_b;
+      if (a.past[b] > (a.c.table_stride << a.c.page_shift) - a.T) over = kFlagCacheOverflow;
+    }
+    if (over != 0 && blockIdx.x == 0) atomicOr(a.status, over);
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPaWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    const long long lo = before + inc - sum;
+    chunk = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)pl.min_chunk);
+    c_lo = min(total, (long long)blockIdx.x * chunk);
+    c_hi = min(total, c_lo + chunk);
+    if (c_lo >= c_hi) return;  // the whole CTA
+    if (c_lo >= lo && c_lo < lo + sum) {
+      long long at = lo;
+      int b = b0;
+      for (;; ++b) {
+        const long long n = (long long)pa_blocks(a, b) * per_b;
+        if (c_lo < at + n || b + 1 >= b1) break;
+        at += n;
+      }
+      s_first[0] = at;
+      s_first[1] = b;
+    }
+    __syncthreads();
+  }
+  int b = (int)s_first[1];
+  int nb = pa_blocks(a, b);
+  int seg = (int)((c_lo - s_first[0]) / nb);  // of sequence b
+  long long seg_lo = s_first[0] + (long long)seg * nb;
+  unsigned bad = 0;
+  unsigned holes = 0;  // bit slot * KB + j: block j of the tile in that stage is not attended
+
+  for (long long cur = c_lo; cur < c_hi;) {
+    // ---- segment (b, kh, rt): blocks [k0, k1) are this CTA's
+    const int kh = seg / pl.nrt, rt = seg - kh * pl.nrt;
+    const int k0 = (int)(cur - seg_lo), k1 = (int)min((long long)nb, c_hi - seg_lo);
+    const int len = pa_len(a, b), past = a.past[b];
+    const int ntile = (k1 - k0 + KB - 1) / KB;  // tiles; warp w takes w, w + kPaWarps, ...
+    const int32_t* table = a.c.table + (size_t)b * a.c.table_stride;
+
+    // page of block j of tile ti (lane j < KB), -1: none
+    auto tile_page = [&](int ti) {
+      const int blk = k0 + ti * KB + lane;
+      if (lane >= KB || ti >= ntile || blk >= k1 || blk * 16 >= len) return -1;
+      const int p = table[(blk * 16) >> a.c.page_shift];
+      if (p < 0 || p >= a.c.num_pages) {
+        bad |= kFlagBadPage;
+        return -1;
+      }
+      return p;
+    };
+    auto issue = [&](int ti, int page, int slot) {
+      holes &= ~(((1u << KB) - 1u) << (slot * KB));
+      holes |= (~__ballot_sync(0xffffffffu, page >= 0) & ((1u << KB) - 1u)) << (slot * KB);
+      if (ti < ntile) {
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const int pg = __shfl_sync(0xffffffffu, page, j);
+          const int pos = (k0 + ti * KB + j) * 16;
+          const int n = pg < 0 ? 0 : min(16, len - pos);  // rows that exist
+          const long long row = pg < 0 ? 0
+                                       : (((long long)pg * a.c.kv_heads + kh) << a.c.page_shift) +
+                                             (pos & ((1 << a.c.page_shift) - 1));
+          const uint32_t dst = stage0 + (uint32_t)(slot * Tile::STAGE + j * Tile::BLOCK);
+          const char* ksrc = static_cast<const char*>(a.c.k) + row * ROW;
+          const char* vsrc = static_cast<const char*>(a.c.v) + row * ROW;
+          constexpr int CPR = ROW / 16;  // chunks per row
+#pragma unroll
+          for (int i = lane; i < 16 * CPR; i += 32) {
+            const int r = i / CPR, c = i % CPR;
+            const uint32_t o = Tile::off(r, c);
+            const size_t so = r < n ? (size_t)i * 16 : 0;
+            pa_cp16(dst + o, ksrc + so, r < n);
+            pa_cp16(dst + 16 * ROW + o, vsrc + so, r < n);
+          }
+          if constexpr (U4) {
+            if (lane < 8) {  // 16 (scale, minimum) pairs of K, then of V: zeros where no row of the chunk exists
+              const int c = lane & 3;
+              const char* s = static_cast<const char*>(lane < 4 ? a.c.k_scale : a.c.v_scale) + row * 4;
+              const bool ok = 4 * c < n;
+              pa_cp16(dst + 32 * ROW + lane * 16, s + (ok ? c * 16 : 0), ok);
+            }
+          }
+        }
+      }
+      pa_commit();
+    };
+
+    int next_page = tile_page(warp);
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) {
+      const int p = next_page;
+      next_page = tile_page(warp + (i + 1) * kPaWarps);
+      issue(warp + i * kPaWarps, p, i);
+    }
+
+    // ---- Q of this segment's rows as the 8-column operand: column n = row g of
+    // each group of 8; 4-bit: channels in the order in which the codes unpack
+    uint32_t qf[NR][KS][2];
+    float q_mul[NR][2], q_sum[NR][2];  // of this lane's columns 2 cq, 2 cq + 1
+    int lim[NR][2];                    // last position those rows see
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = rt * RP + nr * 8 + g;
+      const ACT* qp = nullptr;
+      if (r < R) qp = static_cast<const ACT*>(a.q) + (size_t)(b * a.T + r / G) * a.q_stride + (size_t)(kh * G + r % G) * D;
+      if constexpr (!U4) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[nr][ks][i] = qp != nullptr ? *reinterpret_cast<const uint32_t*>(qp + ks * 16 + i * 8 + 2 * cq) : 0u;
+        q_mul[nr][0] = q_mul[nr][1] = a.scale_log2;
+      } else {
+        // lane cq of a key reads channels [cq D/4, (cq + 1) D/4): 32-bit word w holds
+        // channels 8w .. 8w + 7, pairs (0,4) (1,5) (2,6) (3,7); the second of each two
+        // pairs unpacks to 16 times the code
+        float x[D / 4];
+        float mx = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; i += 8) {
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (qp != nullptr) u = *reinterpret_cast<const uint4*>(qp + cq * (D / 4) + i);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = Act<ACT>::unpack2(w[k]);
+            x[i + 2 * k] = f.x;
+            x[i + 2 * k + 1] = f.y;
+            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            sum += f.x + f.y;
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        // a power of two that brings the largest channel to [1, 2): fp16 then holds
+        // every channel to 2^-24 of it (bf16 queries may lie anywhere)
+        int e = mx > 0.f && mx < INFINITY ? ilogbf(mx) : 0;
+        e = max(-100, min(e, 100));
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float f = exp2f((float)(-e - ((p & 1) ? 4 : 0)));
+            // step 2w + (p >> 1), half p & 1
+            qf[nr][2 * w + (p >> 1)][p & 1] = Act<__half>::pack2(x[8 * w + p] * f, x[8 * w + 4 + p] * f);
+          }
+        const float mul = a.scale_log2 * exp2f((float)e), qs = sum * a.scale_log2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // column c's values are in lanes 4 c ..
+          q_mul[nr][i] = __shfl_sync(0xffffffffu, mul, (2 * cq + i) * 4) * 16777216.f;
+          q_sum[nr][i] = __shfl_sync(0xffffffffu, qs, (2 * cq + i) * 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = rt * RP + nr * 8 + 2 * cq + i;
+        lim[nr][i] = min(len - 1, past + (rr < R ? rr / G : 0));
+      }
+    }
+
+    float o[MT][NR][4], m[NR][2], l[NR][2], om[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) o[mt][nr][0] = o[mt][nr][1] = o[mt][nr][2] = o[mt][nr][3] = 0.f;
+      m[nr][0] = m[nr][1] = -INFINITY;
+      l[nr][0] = l[nr][1] = om[nr][0] = om[nr][1] = 0.f;
+    }
+    int ve = -14;  // 4-bit: exponent that the weights' scales are held relative to
+
+    int slot = 0;
+    for (int ti = warp; ti < ntile; ti += kPaWarps) {
+      pa_wait<NST - 2>();
+      __syncwarp();
+      {
+        const int p = next_page;
+        next_page = tile_page(ti + NST * kPaWarps);
+        issue(ti + (NST - 1) * kPaWarps, p, slot == 0 ? NST - 1 : slot - 1);
+      }
+      const uint32_t st = stage0 + (uint32_t)(slot * Tile::STAGE);
+      const unsigned hole = (holes >> (slot * KB)) & ((1u << KB) - 1u);
+      slot = slot + 1 == NST ? 0 : slot + 1;
+
+      // ---- S^T: 16 positions x 8 rows per block and row group
+      float s[KB][NR][4];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const uint32_t kb = st + (uint32_t)(j * Tile::BLOCK);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) s[j][nr][0] = s[j][nr][1] = s[j][nr][2] = s[j][nr][3] = 0.f;
+        if constexpr (!U4) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t f[4];
+            pa_ldsm4(kb + Tile::off(lane & 15, 2 * ks + (lane >> 4)), f);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) pa_mma<OP>(s[j][nr], f, qf[nr][ks][0], qf[nr][ks][1]);
+          }
+        } else {
+          uint32_t w0[D / 32], w1[D / 32];
+          const int r0 = Tile::key(g), r1 = Tile::key(g + 8);
+          if constexpr (D == 128) {
+            const uint4 u0 = lds_u128(kb + Tile::off(r0, cq)), u1 = lds_u128(kb + Tile::off(r1, cq));
+            w0[0] = u0.x; w0[1] = u0.y; w0[2] = u0.z; w0[3] = u0.w;
+            w1[0] = u1.x; w1[1] = u1.y; w1[2] = u1.z; w1[3] = u1.w;
+          } else {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(kb + r0 * ROW + cq * 8) : "memory");
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(kb + r1 * ROW + cq * 8) : "memory");
+          }
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t x0 = w0[w] >> (8 * h), x1 = w1[w] >> (8 * h);
+              const uint32_t f[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr) pa_mma<OP>(s[j][nr], f, qf[nr][2 * w + h][0], qf[nr][2 * w + h][1]);
+            }
+        }
+      }
+      // ---- scores in the log2 domain, mask, running maximum
+      const int pos0 = (k0 + ti * KB) * 16;
+      float2 vsm[KB][2];  // 4-bit: (scale, minimum) of the lane's two value rows per block
+      const bool tail = hole != 0 || pos0 + KB * 16 > past + 1;  // some row may not see all of the tile
+      float mx[NR][2];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const uint32_t sc = st + (uint32_t)(j * Tile::BLOCK) + 32 * ROW;
+        float2 ksm[2];
+        int key[2] = {g, g + 8};
+        if constexpr (U4) {
+          key[0] = Tile::key(g);
+          key[1] = Tile::key(g + 8);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t u;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(sc + key[i] * 4) : "memory");
+            ksm[i] = __half22float2(*reinterpret_cast<__half2*>(&u));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(sc + 64 + key[i] * 4) : "memory");
+            vsm[j][i] = __half22float2(*reinterpret_cast<__half2*>(&u));
+          }
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float& x = s[j][nr][i];
+            if constexpr (U4) x = fmaf(x * ksm[i >> 1].x, q_mul[nr][i & 1], ksm[i >> 1].y * q_sum[nr][i & 1]);
+            else x *= q_mul[nr][i & 1];
+            if (tail && (((hole >> j) & 1u) != 0 || pos0 + j * 16 + key[i >> 1] > lim[nr][i & 1])) x = -INFINITY;
+          }
+        if (tail && U4) {  // rows behind the sequence share a 16-byte chunk with its last scales
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (pos0 + j * 16 + key[i] >= len) vsm[j][i] = make_float2(0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[nr][i & 1] = fmaxf(mx[nr][i & 1], s[j][nr][i]);
+      float rise = 0.f;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = mx[nr][i];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          mx[nr][i] = fmaxf(m[nr][i], x);
+          if (mx[nr][i] != m[nr][i]) rise = 1.f;
+        }
+      float vf = 1.f, vmul = 1.f;
+      if constexpr (U4) {
+        // the largest scale of the tile, to a power of two: weights times scales then
+        // stay within fp16 whatever the values' size
+        unsigned top = 0;
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) top = max(top, __float_as_uint(fabsf(vsm[j][i].x)));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int e = min((int)(top >> 23) - 127, 16);
+        if (e > ve) {
+          vf = exp2f((float)(ve - e));
+          ve = e;
+          rise = 1.f;
+        }
+        vmul = exp2f((float)-ve);
+      }
+      if (__any_sync(0xffffffffu, rise != 0.f)) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          float al[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            al[i] = mx[nr][i] == -INFINITY ? 1.f : ex2(m[nr][i] - mx[nr][i]);
+            m[nr][i] = mx[nr][i];
+            l[nr][i] *= al[i];
+            om[nr][i] *= al[i];
+            al[i] *= vf;
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            o[mt][nr][0] *= al[0];
+            o[mt][nr][1] *= al[1];
+            o[mt][nr][2] *= al[0];
+            o[mt][nr][3] *= al[1];
+          }
+        }
+      }
+      // ---- weights, and O^T += V^T P^T
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const uint32_t vb = st + (uint32_t)(j * Tile::BLOCK) + 16 * ROW;
+        uint32_t pf[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mm = m[nr][i & 1] == -INFINITY ? 0.f : m[nr][i & 1];
+            p[i] = ex2(s[j][nr][i] - mm);
+            l[nr][i & 1] += p[i];
+            if constexpr (U4) {
+              om[nr][i & 1] = fmaf(p[i], vsm[j][i >> 1].y, om[nr][i & 1]);
+              p[i] *= vsm[j][i >> 1].x * vmul;
+            }
+          }
+          pf[nr][0] = transpose8x8(Act<OP>::pack2(p[0], p[1]));
+          pf[nr][1] = transpose8x8(Act<OP>::pack2(p[2], p[3]));
+        }
+        if constexpr (!U4) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t f[4];
+            pa_ldsm4_t(vb + Tile::off((lane & 7) + ((lane >> 4) << 3), 2 * mt + ((lane >> 3) & 1)), f);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) pa_mma<OP>(o[mt][nr], f, pf[nr][0], pf[nr][1]);
+          }
+        } else {
+          // channels [g D/8, (g + 1) D/8) of the rows that operand columns 2 cq, 2 cq + 1,
+          // 2 cq + 8, 2 cq + 9 hold
+          uint32_t w[4][D / 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = Tile::key(2 * cq + (i & 1) + (i >> 1) * 8);
+            if constexpr (D == 128) {
+              const uint32_t ad = vb + Tile::off(r, g >> 1) + (g & 1) * 8;
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(ad) : "memory");
+            } else {
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i][0]) : "r"(vb + r * ROW + g * 4) : "memory");
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            // nibbles 0..3 and 4..7 of a pair of rows, side by side in 16-bit halves
+            const uint32_t t0 = __byte_perm(w[0][c], w[1][c], 0x5410), u0 = __byte_perm(w[0][c], w[1][c], 0x7632);
+            const uint32_t t1 = __byte_perm(w[2][c], w[3][c], 0x5410), u1 = __byte_perm(w[2][c], w[3][c], 0x7632);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // tile 4 c + k: channels 8 c + k and 8 c + 4 + k of the lane's
+              const uint32_t mask = (k & 1) ? 0x00f000f0u : 0x000f000fu;
+              const int sh = (k >> 1) * 8;
+              const uint32_t f[4] = {(t0 >> sh) & mask, (u0 >> sh) & mask, (t1 >> sh) & mask, (u1 >> sh) & mask};
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr) pa_mma<OP>(o[4 * c + k][nr], f, pf[nr][0], pf[nr][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+    pa_wait<0>();
+
+    // ---- join the warps (the ring is drained; its memory holds their O)
+    float* obuf = reinterpret_cast<float*>(sm);
+    __syncthreads();
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = l[nr][i], y = om[nr][i];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          x += __shfl_xor_sync(0xffffffffu, x, d);
+          y += __shfl_xor_sync(0xffffffffu, y, d);
+        }
+        l[nr][i] = x;
+        om[nr][i] = y;
+        if (g == 0) {
+          s_m[warp][nr * 8 + 2 * cq + i] = m[nr][i];
+          s_l[warp][nr * 8 + 2 * cq + i] = x;
+        }
+      }
+      const float back = U4 ? exp2f((float)(24 + ve)) : 1.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = o[mt][nr][i];
+          int ch = mt * 16 + (i >> 1) * 8 + g;
+          if constexpr (U4) {
+            x = fmaf(x, (mt & 1) ? back * 0.0625f : back, om[nr][i & 1]);
+            ch = g * (D / 8) + (mt >> 2) * 8 + (i >> 1) * 4 + (mt & 3);
+          }
+          obuf[(warp * RP + nr * 8 + 2 * cq + (i & 1)) * OS + ch] = x;
+        }
+    }
+    __syncthreads();
+    const long long seg_hi = seg_lo + nb;
+    const bool whole = seg_lo >= c_lo && seg_hi <= c_hi;
+    const int part = blockIdx.x * 2 + (seg_lo < c_lo ? 0 : 1);
+    const int seg_id = b * per_b + seg;
+    auto store = [&](int r, int c, float4 v) {  // row r of the segment, 4 channels at c
+      const int rr = rt * RP + r;
+      if (rr >= R) return;
+      ACT* dst = static_cast<ACT*>(a.out) + (size_t)(b * a.T + rr / G) * a.out_stride + (size_t)(kh * G + rr % G) * D + c;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(Act<ACT>::pack2(v.x, v.y), Act<ACT>::pack2(v.z, v.w));
+    };
+    for (int i = tid; i < RP * (D / 4); i += kPaThreads) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, s_m[w][r]);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) {
+        // a warp without positions holds nothing; one with NaN scores only keeps them
+        const float f = s_m[w][r] == -INFINITY ? s_l[w][r] : ex2(s_m[w][r] - M);
+        if (f == 0.f) continue;
+        const float4 x = *reinterpret_cast<const float4*>(obuf + (w * RP + r) * OS + c);
+        L += f * s_l[w][r];
+        v.x += f * x.x;
+        v.y += f * x.y;
+        v.z += f * x.z;
+        v.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        store(r, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(pl.part_o + ((size_t)part * RP + r) * D + c) = v;
+        if (c == 0) *reinterpret_cast<float2*>(pl.part_ml + ((size_t)part * RP + r) * 2) = make_float2(M, L);
+      }
+    }
+    if (!whole) {
+      // CTAs first .. last hold a part of this segment
+      const int first = (int)(seg_lo / chunk), last = (int)((seg_hi - 1) / chunk);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomic_add_acq_rel_gpu(pl.counters + seg_id, 1) == last - first;
+      __syncthreads();
+      if (s_last) {
+        if (tid == 0) pl.counters[seg_id] = 0;
+        for (int i = tid; i < RP * (D / 4); i += kPaThreads) {
+          const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+          float M = -INFINITY, L = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = first; k <= last; ++k) {
+            const size_t at = ((size_t)k * 2 + (k == first ? 1 : 0)) * RP + r;
+            const float mk = ld_cg(pl.part_ml + at * 2), lk = ld_cg(pl.part_ml + at * 2 + 1);
+            const float4 x = ld_cg4(pl.part_o + at * D + c);
+            if (mk == -INFINITY && lk == 0.f) continue;
+            const float mn = fmaxf(M, mk), f0 = ex2(M - mn), f1 = ex2(mk - mn);
+            L = L * f0 + lk * f1;
+            v.x = v.x * f0 + x.x * f1;
+            v.y = v.y * f0 + x.y * f1;
+            v.z = v.z * f0 + x.z * f1;
+            v.w = v.w * f0 + x.w * f1;
+            M = mn;
+          }
+          const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+          store(r, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        }
+      }
+    }
+    __syncthreads();  // obuf and s_m are free for the next segment
+
+    // ---- the next segment
+    cur = seg_hi;
+    seg_lo = seg_hi;
+    if (++seg == per_b) {
+      seg = 0;
+      if (++b < B) nb = pa_blocks(a, b);
+    }
+  }
+  if (bad != 0) atomicOr(a.status, bad);
+}
+
+static int pa_rows(int heads, int kv_heads, int T) { return heads / kv_heads * T; }
+
+struct PaWs {
+  size_t counters, part_o, part_ml, total;
+  int nr, nrt, grid, min_chunk;
+};
+// Blocks of 16 positions a CTA takes at least: one tile a warp.
+static int pa_min_chunk(const PagedView& c) {
+  if (c.u4) return kPaWarps * (c.head_dim == 64 ? PaTile<64, true>::KB : PaTile<128, true>::KB);
+  return kPaWarps * (c.head_dim == 64 ? PaTile<64, false>::KB : PaTile<128, false>::KB);
+}
+static PaWs pa_ws(const PagedView& c, int heads, int batch, int T, int num_sms) {
+  PaWs w;
+  const int R = pa_rows(heads, c.kv_heads, T);
+  w.nr = R <= 8 ? 1 : 2;
+  w.nrt = (R + 8 * w.nr - 1) / (8 * w.nr);
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  // as many CTAs as stay resident, fewer where even full tables would not feed them
+  w.min_chunk = pa_min_chunk(c);
+  const long long most = (((long long)c.table_stride << c.page_shift) / 16) * batch * c.kv_heads * w.nrt;
+  const long long ctas = (most + w.min_chunk - 1) / w.min_chunk;
+  w.grid = (int)(ctas < (long long)num_sms * kPaCtasPerSm ? ctas : (long long)num_sms * kPaCtasPerSm);
+  const size_t slots = (size_t)w.grid * 2 * 8 * w.nr;
+  w.counters = 256;
+  w.part_ml = w.counters + up((size_t)batch * c.kv_heads * w.nrt * 4);
+  w.part_o = w.part_ml + up(slots * 2 * 4);
+  w.total = w.part_o + up(slots * c.head_dim * 4);
+  return w;
+}
+
+size_t paged_attention_ws_bytes(const PagedView& c, int heads, int batch, int T, int num_sms) {
+  return pa_ws(c, heads, batch, T, num_sms).total;
+}
+
+template <typename ACT, int D, bool U4, int NR>
+static cudaError_t attention_launch(const PagedAttnArgs& a, const PaPlan& pl, int grid, cudaStream_t st) {
+  using Tile = PaTile<D, U4>;
+  constexpr int merge = kPaWarps * 8 * NR * (D + 4) * 4;
+  constexpr int smem = Tile::SMEM > merge ? Tile::SMEM : merge;
+  const auto kernel = paged_attention_kernel<ACT, D, U4, NR>;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!((ready.load(std::memory_order_relaxed) >> (dev & 63)) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, a, pl);
+}
 
 template <typename ACT, int D>
-static cudaError_t attention_launch(const PagedAttnArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.batch * a.T), (unsigned)a.heads);
-  cfg.blockDim = dim3(kSimpleThreads);
-  cfg.stream = st;
-  if (a.c.u4) return cudaLaunchKernelEx(&cfg, paged_attention_kernel<ACT, D, true>, a);
-  return cudaLaunchKernelEx(&cfg, paged_attention_kernel<ACT, D, false>, a);
+static cudaError_t attention_pick(const PagedAttnArgs& a, const PaPlan& pl, int nr, int grid, cudaStream_t st) {
+  if (a.c.u4) return nr == 1 ? attention_launch<ACT, D, true, 1>(a, pl, grid, st)
+                             : attention_launch<ACT, D, true, 2>(a, pl, grid, st);
+  return nr == 1 ? attention_launch<ACT, D, false, 1>(a, pl, grid, st)
+                 : attention_launch<ACT, D, false, 2>(a, pl, grid, st);
 }
 
-cudaError_t launch_paged_attention(const PagedAttnArgs& a, void*, int, cudaStream_t st) {
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, int num_sms, cudaStream_t st) {
+  const PaWs w = pa_ws(a.c, a.heads, a.batch, a.T, num_sms);
+  char* base = static_cast<char*>(ws);
+  PaPlan pl;
+  pl.nrt = w.nrt;
+  pl.min_chunk = w.min_chunk;
+  pl.counters = reinterpret_cast<int*>(base + w.counters);
+  pl.part_ml = reinterpret_cast<float*>(base + w.part_ml);
+  pl.part_o = reinterpret_cast<float*>(base + w.part_o);
   if (a.c.act == ActKind::F16)
-    return a.c.head_dim == 64 ? attention_launch<__half, 64>(a, st) : attention_launch<__half, 128>(a, st);
-  return a.c.head_dim == 64 ? attention_launch<__nv_bfloat16, 64>(a, st) : attention_launch<__nv_bfloat16, 128>(a, st);
+    return a.c.head_dim == 64 ? attention_pick<__half, 64>(a, pl, w.nr, w.grid, st)
+                              : attention_pick<__half, 128>(a, pl, w.nr, w.grid, st);
+  return a.c.head_dim == 64 ? attention_pick<__nv_bfloat16, 64>(a, pl, w.nr, w.grid, st)
+                            : attention_pick<__nv_bfloat16, 128>(a, pl, w.nr, w.grid, st);
 }
 
 }  // namespace ds
