@@ -156,7 +156,7 @@ def test_append_refusals(lib, kw, code):  # noqa: F811
 @pytest.mark.parametrize("kw,code", [
     (dict(heads=3), ds.DS_ERR_INVALID_ARG), (dict(heads=0), ds.DS_ERR_INVALID_ARG), (dict(batch=0), ds.DS_ERR_INVALID_ARG),
     (dict(batch=1 << 17), ds.DS_ERR_INVALID_ARG), (dict(T=0), ds.DS_ERR_UNSUPPORTED), (dict(T=17), ds.DS_ERR_UNSUPPORTED),
-    (dict(scale=float("inf")), ds.DS_ERR_INVALID_ARG), (dict(scale=float("nan")), ds.DS_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), ds.DS_ERR_INVALID_ARG), (dict(scale=0.0), ds.DS_ERR_INVALID_ARG), (dict(scale=float("nan")), ds.DS_ERR_INVALID_ARG),
     (dict(q=None), ds.DS_ERR_INVALID_ARG), (dict(out=P), ds.DS_ERR_INVALID_ARG), (dict(qs=255), ds.DS_ERR_INVALID_ARG),
     (dict(os=128), ds.DS_ERR_INVALID_ARG), (dict(past=None), ds.DS_ERR_INVALID_ARG),
 ])
@@ -170,7 +170,8 @@ def test_attention_refusals(lib, kw, code):  # noqa: F811
     (dict(heads=5), ds.DS_ERR_INVALID_ARG), (dict(kv=0), ds.DS_ERR_INVALID_ARG), (dict(nq=-1), ds.DS_ERR_INVALID_ARG),
     (dict(nk=-1), ds.DS_ERR_INVALID_ARG), (dict(nq=1 << 25), ds.DS_ERR_INVALID_ARG), (dict(cu_q=None), ds.DS_ERR_INVALID_ARG),
     (dict(cu_k=C.c_void_p(4097)), ds.DS_ERR_INVALID_ARG), (dict(batch=0), ds.DS_ERR_INVALID_ARG),
-    (dict(scale=float("nan")), ds.DS_ERR_INVALID_ARG), (dict(q=None), ds.DS_ERR_INVALID_ARG), (dict(k=None), ds.DS_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), ds.DS_ERR_INVALID_ARG), (dict(scale=-0.1), ds.DS_ERR_INVALID_ARG),
+    (dict(q=None), ds.DS_ERR_INVALID_ARG), (dict(k=None), ds.DS_ERR_INVALID_ARG),
     (dict(out=P), ds.DS_ERR_INVALID_ARG), (dict(ks=120), ds.DS_ERR_INVALID_ARG), (dict(os=260), ds.DS_ERR_INVALID_ARG),
     (dict(ws=None), ds.DS_ERR_INVALID_ARG), (dict(ws_bytes=64), ds.DS_ERR_WORKSPACE),
 ])

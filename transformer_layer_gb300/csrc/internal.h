@@ -199,6 +199,10 @@ bool dense_make_plan(ActKind ak, int N, int K, int M, int num_sms, int max_smem,
 // Encodes the tile tensor map of a row-major [rows][cols] 16-bit matrix
 // (box 128 rows x kc, or ntok rows x kc for activation operands).
 bool encode_tile_map(void* map128, const void* base, int rows, int cols, int box_rows, int kc);
+// Encodes the tensor map of a packed 16-bit tensor [tokens][cols] whose rows
+// are `stride` elements apart (box box_rows tokens x box_cols columns).
+bool encode_packed_map(void* map128, const void* base, int tokens, long long stride, int cols, int box_rows,
+                       int box_cols);
 cudaError_t launch_dense(Region r, ActKind ak, const DenseArgs& a, const void* xmap_hi, const void* xmap_lo,
                          cudaStream_t st, bool pdl);
 cudaError_t launch_ln_prep(ActKind ak, const LnPrepArgs& a, cudaStream_t st, bool pdl);

@@ -250,7 +250,7 @@ ds_status ds_paged_attention(const ds_paged_cache* cache, const void* q, void* o
     return fail(DS_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads, up to 65535");
   if (batch < 1 || batch > 65535) return fail(DS_ERR_INVALID_ARG, "batch must be in 1 .. 65535");
   if (new_tokens < 1 || new_tokens > 16) return fail(DS_ERR_UNSUPPORTED, "new_tokens must be in 1 .. 16");
-  if (!std::isfinite(scale)) return fail(DS_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite(scale) || scale <= 0.f) return fail(DS_ERR_INVALID_ARG, "scale must be positive and finite");
   DS_TRY(check_packed(q, q_stride, heads, cache->head_dim));
   DS_TRY(check_packed(out, out_stride, heads, cache->head_dim));
   if (q == out) return fail(DS_ERR_INVALID_ARG, "out must not alias q");
@@ -295,7 +295,7 @@ ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void*
     return fail(DS_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads, up to 65535");
   DS_TRY(check_batch(q_tokens, batch, cu_q, cu_k));
   if (k_tokens < 0 || k_tokens > (1 << 24)) return fail(DS_ERR_INVALID_ARG, "k_tokens must be in 0 .. 2^24");
-  if (!std::isfinite(scale)) return fail(DS_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite(scale) || scale <= 0.f) return fail(DS_ERR_INVALID_ARG, "scale must be positive and finite");
   DS_TRY(check_ws(workspace, ws_bytes, prompt_attention_ws_bytes(heads, batch, q_tokens)));
   if (q_tokens == 0) return DS_OK;
   DS_TRY(check_packed(q, q_stride, heads, head_dim));
@@ -332,7 +332,7 @@ ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void*
   a.scale_log2 = scale_log2(scale);
   a.status = static_cast<unsigned*>(workspace);
   return launched(launch_prompt_attention(a, workspace, sms, static_cast<cudaStream_t>(stream)),
-                  "prompt attention launch", 1);
+                  "prompt attention launch", 2);
 }
 
 }  // extern "C"

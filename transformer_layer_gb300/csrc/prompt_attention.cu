@@ -1,83 +1,579 @@
 // Causal attention over packed prompts of different lengths, grouped heads
 // (ds_prompt_attention).
 //
-// Mathematics, per (query i of sequence b, head h): s_j = scale q_i . k_j for
-// keys j <= Lk - Lq + i of the same sequence, out = softmax(s) V.
+// Page cited: "DeepSpeed Inference 内核优化深度解析：多 GPU 自适应并行、算子融合推理内核
+// 与 MoQ 量化支持", §3.2 region 2 (the attention products and the softmax between
+// them in one kernel); packed sequences and grouped heads are this library's
+// own extension.
 //
-// First form: one CTA per (query, head), its warps take every 4th key with a
-// running maximum and sum each, and meet in shared memory.
+// Mathematics, per (query i of sequence b, head h): s_j = scale q_i . k_j for
+// keys j <= Lk - Lq + i of the same sequence, out = softmax(s) V, in one pass
+// over the keys: with a running reference m of the row's scores,
+//   l = sum_j 2^(c s_j - c m),  O = sum_j 2^(c s_j - c m) v_j,  out = O / l,
+// c = scale log2(e).  m follows the row's maximum only when it has fallen
+// 2^8 behind (then l and O are multiplied once): any m gives the same quotient,
+// and weights up to 256 fit fp16 and bf16 with the same relative rounding.
+//
+// Bound: the tensor cores (4 d products per visible pair).  A CTA works on two
+// tiles of 128 queries against the same stream of 128-key blocks:
+//  * S = Q K^T and O += P V are tcgen05.mma with M = 128, N = 128 or d, the
+//    accumulators S0 S1 O0 O1 in tensor memory (512 columns); P goes back to
+//    tensor memory over S's columns as the A operand, so nothing but Q, K and V
+//    passes through shared memory;
+//  * warps 0-3 and 4-7 hold one query row a thread (no shuffles) and run the
+//    softmax of tile 0 and 1 in turn with the other tile's products;
+//  * one warp loads (TMA, ring of 128-key tiles of K and V), two warps issue the
+//    products, one per tile: S(j + 1) follows P V(j) in the same issue order, so
+//    its completion also tells the softmax that O is at rest.
+// With an even number of query heads per key head the two tiles are the same
+// queries of two heads (equal work, K and V read once for both), else two
+// neighbouring tiles of one head.
+// The last block of a sequence may hold rows of the next one: scores are masked
+// by position, and V rows behind the sequence are zero-filled (that block of V
+// comes by cp.async), so that nothing of one sequence reaches another.
+//
+// Split: a first small kernel lists the query tiles, longest first; CTAs (one
+// per SM) take items of (tile, head pair) in alternating order.
+#include <cuda.h>
+
+#include <atomic>
+#include <cstring>
+#include <type_traits>
+
 #include "paged.cuh"
+#include "tcgen05.cuh"
 
 namespace ds {
 
-constexpr int kSimplePromptThreads = 128;
+constexpr int kPrLoadWarp = 8;   // after the softmax warps: 0-3 of tile 0, 4-7 of tile 1
+constexpr int kPrMmaWarp = 9;    // and 10
+constexpr int kPrThreads = 11 * 32;
+constexpr int kPrRows = 128;     // queries per tile, keys per block
+constexpr float kPrBehind = 8.f; // log2 a row's maximum may be ahead of its reference
 
-template <typename ACT, int D>
-__global__ void __launch_bounds__(kSimplePromptThreads) prompt_attention_kernel(const PromptAttnArgs a) {
-  constexpr int C = D / 32, W = kSimplePromptThreads / 32;
-  __shared__ float so[W][D], sm[W], sl[W];
-  const int row = blockIdx.x, h = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = find_sequence(a.cu_q, a.batch, row);
-  if (b >= a.batch) return;
-  const int kh = h / (a.heads / a.kv_heads);
-  const int k0 = max(0, a.cu_k[b]), k1 = min(a.cu_k[b + 1], a.k_tokens);
-  const int n = min(k1 - k0, (k1 - k0) - (a.cu_q[b + 1] - a.cu_q[b]) + (row - a.cu_q[b]) + 1);
-  const ACT* q = static_cast<const ACT*>(a.q) + (size_t)row * a.q_stride + (size_t)h * D + lane * C;
-  float qv[C], o[C], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    qv[i] = Act<ACT>::to_f(q[i]) * a.scale_log2;
-    o[i] = 0.f;
-  }
-  for (int j = warp; j < n; j += W) {
-    const ACT* k = static_cast<const ACT*>(a.k) + (size_t)(k0 + j) * a.k_stride + (size_t)kh * D + lane * C;
-    const ACT* v = static_cast<const ACT*>(a.v) + (size_t)(k0 + j) * a.v_stride + (size_t)kh * D + lane * C;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) s += qv[i] * Act<ACT>::to_f(k[i]);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * al + p;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = o[i] * al + p * Act<ACT>::to_f(v[i]);
-    m = mn;
-  }
-#pragma unroll
-  for (int i = 0; i < C; ++i) so[warp][lane * C + i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
+// One entry of the work list: a tile (or two neighbouring ones) of a sequence.
+struct PromptItem {
+  int q0;     // first packed query row
+  int rows;   // queries from there on (up to 128, or 256 for two tiles)
+  int k0;     // first packed key row of the sequence
+  int lk;     // its keys
+  int lim;    // last key that the first query sees (may be negative)
+  int pad[3];
+};
+struct PromptList {
+  int count;
+  int pad[63];
+};
+
+// Lists the tiles of `unit` queries of all sequences, most key blocks first
+// (counting sort, the last bucket for 1023 blocks or more).
+__global__ void __launch_bounds__(1024) prompt_list_kernel(const PromptAttnArgs a, int unit, PromptList* list,
+                                                           PromptItem* items, int most) {
+  __shared__ int hist[1024], s_warp[32];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  hist[tid] = 0;
   __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY;
-    for (int w = 0; w < W; ++w) M = fmaxf(M, sm[w]);
-    float L = 0.f, O = 0.f;
-    for (int w = 0; w < W; ++w) {
-      const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - M);
-      L += f * sl[w];
-      O += f * so[w][threadIdx.x];
+  auto each = [&](auto&& f) {
+    for (int b = warp; b < a.batch; b += 32) {
+      const int q0 = max(0, a.cu_q[b]), q1 = min(a.cu_q[b + 1], a.q_tokens);
+      const int k0 = max(0, a.cu_k[b]), lk = max(0, min(a.cu_k[b + 1], a.k_tokens) - k0);
+      const int lq = q1 - q0;
+      for (int t = lane; t * unit < lq; t += 32) {
+        PromptItem it = {};
+        it.q0 = q0 + t * unit;
+        it.rows = min(unit, lq - t * unit);
+        it.k0 = k0;
+        it.lk = lk;
+        it.lim = lk - lq + t * unit;
+        const int seen = max(0, min(lk, it.lim + it.rows));
+        f(it, 1023 - min(1023, (seen + kPrRows - 1) / kPrRows));
+      }
     }
-    static_cast<ACT*>(a.out)[(size_t)row * a.out_stride + (size_t)h * D + threadIdx.x] =
-        Act<ACT>::from_f(L > 0.f ? O / L : 0.f);
+  };
+  each([&](const PromptItem&, int key) { atomicAdd(&hist[key], 1); });
+  __syncthreads();
+  const int n = hist[tid];
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
   }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  hist[tid] = before + inc - n;
+  if (tid == 1023) list->count = min(before + inc, most);
+  __syncthreads();
+  each([&](const PromptItem& it, int key) {
+    const int at = atomicAdd(&hist[key], 1);
+    if (at < most) items[at] = it;
+  });
 }
 
-size_t prompt_attention_ws_bytes(int, int, int) { return 256; }
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// (the loaded registers are tied to the wait, so that no use of them moves before it)
+__device__ __forceinline__ void tmem_wait_ld32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+__device__ __forceinline__ float pr_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+// (x0, x1) * c + d and (a0, a1) + (b0, b1), two lanes of one instruction
+__device__ __forceinline__ void fma2(float& x0, float& x1, float c, float d) {
+  asm("{\n .reg .b64 x, c, d;\n mov.b64 x, {%0, %1};\n mov.b64 c, {%2, %2};\n mov.b64 d, {%3, %3};\n"
+      " fma.rn.f32x2 x, x, c, d;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mul.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b));
+}
+
+// B operand with N contiguous (V as [keys][d]: rows of 128 bytes are 64 values of
+// d, 8 keys a 1024-byte group, the next 64 values of d `lead` bytes on).
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t lead) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
+template <int D>
+struct PromptSmem {
+  static constexpr int TILE = kPrRows * D * 2;  // bytes of a tile of Q, K or V
+  static constexpr int NST = D == 128 ? 5 : 8;  // ring stages
+  static constexpr int Q = 0;
+  static constexpr int RING = 2 * TILE;
+  static constexpr int BARS = RING + NST * TILE;
+  static constexpr int TOTAL = BARS + 256 + 1024;  // and the alignment of the base
+};
+
+// A CTA's k-th item of n: rounds of `grid` items taken in alternating direction,
+// so that the longer items of one round meet the shorter ones of the next.
+__device__ __forceinline__ long long prompt_item(int k, long long n) {
+  const int g = gridDim.x, c = blockIdx.x;
+  const long long i = (long long)k * g + ((k & 1) ? g - 1 - c : c);
+  return i < n ? i : -1;
+}
 
 template <typename ACT, int D>
-static cudaError_t prompt_launch(const PromptAttnArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.q_tokens, (unsigned)a.heads);
-  cfg.blockDim = dim3(kSimplePromptThreads);
-  cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, prompt_attention_kernel<ACT, D>, a);
+__global__ void __launch_bounds__(kPrThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                            const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptAttnArgs a,
+                            const PromptList* list, const PromptItem* items, int pair_heads) {
+  using SM = PromptSmem<D>;
+  constexpr int NST = SM::NST, TILE = SM::TILE;
+  constexpr bool kBf16 = std::is_same<ACT, __nv_bfloat16>::value;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint32_t s_tmem;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bars = base + SM::BARS;
+  auto full = [&](int i) { return bars + 8u * i; };
+  auto empty = [&](int i) { return bars + 8u * (NST + i); };
+  auto q_full = [&](int t) { return bars + 8u * (2 * NST + t); };
+  auto q_empty = [&](int t) { return bars + 8u * (2 * NST + 2 + t); };
+  auto s_full = [&](int t) { return bars + 8u * (2 * NST + 4 + t); };
+  auto p_full = [&](int t) { return bars + 8u * (2 * NST + 6 + t); };
+  auto o_full = [&](int t) { return bars + 8u * (2 * NST + 8 + t); };
+  auto done = [&](int t) { return bars + 8u * (2 * NST + 10 + t); };
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 2);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 1);
+      mbar_init(q_empty(t), 1);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(o_full(t), 1);
+      mbar_init(done(t), 1);
+    }
+    mbar_init_fence();
+  }
+  if (warp == kPrMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+
+  const int group = a.heads / a.kv_heads;
+  const int hp = pair_heads ? a.heads / 2 : a.heads;  // items per list entry
+  const long long n_items = (long long)list->count * hp;
+  bool dead = false;  // a wait of this warp gave up: nothing more is waited for or issued
+
+  // What an item means for tile t.
+  struct Tile {
+    int q0, rows, head, lim, n;
+  };
+  auto tile_of = [&](const PromptItem& it, int h, int t) {
+    Tile r;
+    const int skip = pair_heads ? 0 : t * kPrRows;
+    r.q0 = it.q0 + skip;
+    r.rows = max(0, min(kPrRows, it.rows - skip));
+    r.head = pair_heads ? 2 * h + t : h;
+    r.lim = it.lim + skip;
+    const int seen = r.rows > 0 ? max(0, min(it.lk, r.lim + r.rows)) : 0;
+    r.n = (seen + kPrRows - 1) / kPrRows;
+    return r;
+  };
+
+  if (warp == kPrLoadWarp) {
+    // ------------------------------------------------------------ loads
+    int st = 0;
+    uint32_t ph = 0, qph = 0;
+    const uint64_t keep = l2_evict_normal_policy();
+    auto next_stage = [&]() {
+      if (++st == NST) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    int used = 0;
+    for (int k = 0;; ++k) {
+      const long long i = prompt_item(k, n_items);
+      if (i < 0) break;
+      const PromptItem it = items[i / hp];
+      const Tile t0 = tile_of(it, (int)(i % hp), 0), t1 = tile_of(it, (int)(i % hp), 1);
+      const int n = max(t0.n, t1.n);
+      const int kvh = t0.head / group;
+      for (int j = 0; j < n; ++j) {
+        if (j == 0) {
+          for (int t = 0; t < 2; ++t) {
+            const Tile& tt = t ? t1 : t0;
+            if (!dead) dead = !mbar_wait(q_empty(t), qph ^ 1, a.status);
+            dead = __any_sync(0xffffffffu, dead);
+            if (lane == 0 && !dead) {
+              mbar_arrive_expect_tx(q_full(t), TILE);
+              tma_load_3d(base + SM::Q + t * TILE, &mq, 0, min(tt.q0, a.q_tokens - 1), tt.head * (D / 64), q_full(t),
+                          keep);
+            }
+          }
+          qph ^= 1;
+        }
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!dead) dead = !mbar_wait(empty(st), ph ^ 1, a.status);
+          dead = __any_sync(0xffffffffu, dead);
+          if (!dead) {
+            const uint32_t dst = base + SM::RING + st * TILE;
+            const int row0 = it.k0 + j * kPrRows, valid = it.lk - j * kPrRows;
+            if (kv == 0 || valid >= kPrRows) {
+              if (lane == 0) {
+                mbar_arrive_expect_tx(full(st), TILE);
+                tma_load_3d(dst, kv ? &mv : &mk, 0, row0, kvh * (D / 64), full(st), keep);
+              }
+            } else {
+              // the sequence ends in this block: rows behind it are zeros
+              const ACT* src = static_cast<const ACT*>(a.v) + (size_t)row0 * a.v_stride + (size_t)kvh * D;
+              for (int c = lane; c < kPrRows * (D / 8); c += 32) {
+                const int r = c / (D / 8), ch = c % (D / 8);
+                const uint32_t at = dst + (uint32_t)((ch >> 3) * (kPrRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                const ACT* from = src + (r < valid ? (size_t)r * a.v_stride + ch * 8 : 0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(at), "l"(from),
+                             "r"(r < valid ? 16 : 0)
+                             : "memory");
+              }
+              asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(full(st)) : "memory");
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full(st));
+            }
+            used = max(used, st + 1);
+            next_stage();
+          }
+        }
+      }
+    }
+    // every copy has landed before the CTA may end (a reader that gave up did not wait)
+    for (int i = 0; i < used; ++i) {
+      const uint32_t p = i < st ? ph : ph ^ 1;  // parity of the stage's last use
+      mbar_wait(full(i), p, a.status);
+    }
+  } else if (warp == kPrMmaWarp || warp == kPrMmaWarp + 1) {
+    // ------------------------------------------------------------ products
+    const int t = warp - kPrMmaWarp;
+    const uint32_t idesc_s = umma_idesc(kBf16, kPrRows), idesc_o = umma_idesc(kBf16, D) | (1u << 16);
+    const uint32_t ts = tmem + (uint32_t)(t * kPrRows), to = tmem + (uint32_t)(2 * kPrRows + t * kPrRows);
+    int st = 0;
+    uint32_t ph = 0, qph = 0, pph = 0;
+    auto next_stage = [&]() {
+      if (++st == NST) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    auto take = [&]() {  // the ring's next stage is full
+      if (!dead) dead = !mbar_wait(full(st), ph, a.status);
+      dead = __any_sync(0xffffffffu, dead);
+    };
+    for (int k = 0;; ++k) {
+      const long long i = prompt_item(k, n_items);
+      if (i < 0) break;
+      const PromptItem it = items[i / hp];
+      const Tile tl = tile_of(it, (int)(i % hp), t), tr = tile_of(it, (int)(i % hp), 1 - t);
+      const int n = tl.n, nkv = max(n, tr.n);
+      if (nkv == 0) continue;
+      if (!dead) dead = !mbar_wait(q_full(t), qph, a.status);
+      qph ^= 1;
+      const uint64_t dq = umma_desc_sw128(base + SM::Q + t * TILE);
+      auto product_s = [&](int j) {  // S = Q K_j^T from the ring's stage; releases it
+        take();
+        if (lane == 0 && !dead) {
+          tc_fence_after();
+          const uint64_t dk = umma_desc_sw128(base + SM::RING + st * TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t step = (uint64_t)(((kk >> 2) * (kPrRows * 128) + (kk & 3) * 32) >> 4);
+            umma_f16(ts, dq + step, dk + step, idesc_s, kk > 0);
+          }
+          umma_commit(s_full(t));
+          umma_commit(empty(st));
+          if (j == n - 1) umma_commit(q_empty(t));
+        }
+        next_stage();
+      };
+      auto pass = [&]() {  // a stage that only the other tile uses
+        take();
+        if (lane == 0 && !dead) mbar_arrive(empty(st));
+        next_stage();
+      };
+      if (n == 0 && lane == 0 && !dead) mbar_arrive(q_empty(t));
+      if (n > 0) product_s(0);
+      else pass();
+      for (int j = 0; j < nkv; ++j) {
+        if (j >= n) {
+          pass();  // V_j
+          if (j + 1 < nkv) pass();
+          continue;
+        }
+        take();  // V_j
+        if (!dead) dead = !mbar_wait(p_full(t), pph, a.status);
+        dead = __any_sync(0xffffffffu, dead);
+        pph ^= 1;
+        if (lane == 0 && !dead) {
+          tc_fence_after();
+          if (it.lk - j * kPrRows < kPrRows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          const uint64_t dv = umma_desc_mn_sw128(base + SM::RING + st * TILE, kPrRows * 128);
+#pragma unroll
+          for (int kk = 0; kk < kPrRows / 16; ++kk)
+            umma_f16_tmem_a(to, ts + (uint32_t)(kk * 8), dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (j > 0 || kk > 0));
+          if (j == n - 1) umma_commit(o_full(t));
+          umma_commit(empty(st));
+        }
+        next_stage();
+        if (j + 1 < n) product_s(j + 1);
+        else if (j + 1 < nkv) pass();
+      }
+    }
+    if (lane == 0) umma_commit(done(t));
+    mbar_wait(done(t), 0, a.status);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + (uint32_t)(t * kPrRows);
+    const uint32_t to = tmem + lanes + (uint32_t)(2 * kPrRows + t * kPrRows);
+    const int row = 32 * (warp & 3) + lane;
+    const float c = a.scale_log2;
+    uint32_t sph = 0, oph = 0;
+    for (int k = 0;; ++k) {
+      const long long i = prompt_item(k, n_items);
+      if (i < 0) break;
+      const PromptItem it = items[i / hp];
+      const Tile tl = tile_of(it, (int)(i % hp), t);
+      float m = -INFINITY, l = 0.f;
+      const int lim = min(it.lk - 1, tl.lim + row);  // last key this row sees
+      for (int j = 0; j < tl.n; ++j) {
+        if (!dead) dead = !mbar_wait(s_full(t), sph, a.status);
+        dead = __any_sync(0xffffffffu, dead);
+        sph ^= 1;
+        if (dead) continue;
+        tc_fence_after();
+        float s[kPrRows];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_nowait(ts + (uint32_t)(32 * q), s + 32 * q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait_ld32(s + 32 * q);
+        // some row of the tile sees less than the whole block
+        if (min(it.lk - 1, tl.lim) < (j + 1) * kPrRows - 1) {
+          const int last = lim - j * kPrRows;
+#pragma unroll
+          for (int x = 0; x < kPrRows; ++x)
+            if (x > last) s[x] = -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(s[q], s[q + 4]);
+#pragma unroll
+        for (int x = 8; x < kPrRows; x += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], fmaxf(s[x + q], s[x + q + 4]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (__any_sync(0xffffffffu, (top - m) * c > kPrBehind)) {
+          const float mn = fmaxf(m, top);
+          const float al = mn == -INFINITY ? 1.f : pr_ex2((m - mn) * c);
+          m = mn;
+          l *= al;
+          if (j > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              float o[32];
+              tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) mul2(o[x], o[x + 1], al);
+              tmem_st32(to + (uint32_t)(32 * q), reinterpret_cast<uint32_t(&)[32]>(o));
+            }
+          }
+        }
+        const float mc = m == -INFINITY ? 0.f : -m * c;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 4) {
+            float* v = s + 64 * h + x;
+            fma2(v[0], v[1], c, mc);
+            fma2(v[2], v[3], c, mc);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = pr_ex2(v[y]);
+            add2(l0, l1, v[0], v[1]);
+            add2(l2, l3, v[2], v[3]);
+            p[x / 2] = Act<ACT>::pack2(v[0], v[1]);
+            p[x / 2 + 1] = Act<ACT>::pack2(v[2], v[3]);
+          }
+          tmem_st32(ts + (uint32_t)(32 * h), p);
+        }
+        l += (l0 + l1) + (l2 + l3);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
+      }
+      // ---- out = O / l
+      const bool keeps = row < tl.rows;
+      ACT* dst = static_cast<ACT*>(a.out) + (size_t)(tl.q0 + row) * a.out_stride + (size_t)tl.head * D;
+      if (tl.n > 0) {
+        if (!dead) dead = !mbar_wait(o_full(t), oph, a.status);
+        dead = __any_sync(0xffffffffu, dead);
+        oph ^= 1;
+        if (dead) continue;
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const bool none = lim < 0;  // O holds the products of zero weights: nothing to divide
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          float o[32];
+          tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
+          tmem_wait_ld32(o);
+          if (keeps) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = none ? 0u : Act<ACT>::pack2(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
+              *reinterpret_cast<uint4*>(dst + 32 * q + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();
+      } else if (keeps) {
+#pragma unroll
+        for (int x = 0; x < D; x += 8) *reinterpret_cast<uint4*>(dst + x) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kPrMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void*, int, cudaStream_t st) {
-  if (a.act == ActKind::F16) return a.head_dim == 64 ? prompt_launch<__half, 64>(a, st) : prompt_launch<__half, 128>(a, st);
-  return a.head_dim == 64 ? prompt_launch<__nv_bfloat16, 64>(a, st) : prompt_launch<__nv_bfloat16, 128>(a, st);
+static bool pairs_heads(int heads, int kv_heads) { return (heads / kv_heads) % 2 == 0; }
+// List entries that q_tokens queries of `batch` sequences can make, either way of pairing tiles.
+static size_t prompt_most(int batch, int tokens) { return (size_t)tokens / kPrRows + (size_t)batch + 1; }
+
+size_t prompt_attention_ws_bytes(int, int batch, int tokens) {
+  return 256 + sizeof(PromptList) + ((prompt_most(batch, tokens) * sizeof(PromptItem) + 255) & ~(size_t)255);
+}
+
+template <typename ACT, int D>
+static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st) {
+  const auto kernel = prompt_attention_kernel<ACT, D>;
+  static std::atomic<unsigned long long> ready{0};  // devices on which the limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!((ready.load(std::memory_order_relaxed) >> (dev & 63)) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<D>::TOTAL);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  alignas(64) CUtensorMap m[3];
+  std::memset(m, 0, sizeof(m));
+  const int nk = a.k_tokens > 0 ? a.k_tokens : 1;  // no keys: the maps are never used
+  const void *kp = a.k_tokens > 0 ? a.k : a.q, *vp = a.k_tokens > 0 ? a.v : a.q;
+  if (!encode_packed_map(&m[0], a.q, a.q_tokens, a.q_stride, a.heads * D, kPrRows, D) ||
+      !encode_packed_map(&m[1], kp, nk, a.k_tokens > 0 ? a.k_stride : a.q_stride, a.kv_heads * D, kPrRows, D) ||
+      !encode_packed_map(&m[2], vp, nk, a.k_tokens > 0 ? a.v_stride : a.q_stride, a.kv_heads * D, kPrRows, D))
+    return cudaErrorInvalidValue;
+  PromptList* list = reinterpret_cast<PromptList*>(static_cast<char*>(ws) + 256);
+  PromptItem* items = reinterpret_cast<PromptItem*>(list + 1);
+  const int pair = pairs_heads(a.heads, a.kv_heads);
+  const int most = (int)prompt_most(a.batch, a.q_tokens);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  e = cudaLaunchKernelEx(&cfg, prompt_list_kernel, a, pair ? kPrRows : 2 * kPrRows, list, items, most);
+  if (e != cudaSuccess) return e;
+  const long long ctas = (long long)most * (pair ? a.heads / 2 : a.heads);
+  cfg.gridDim = dim3((unsigned)(ctas < num_sms ? ctas : num_sms));
+  cfg.blockDim = dim3(kPrThreads);
+  cfg.dynamicSmemBytes = PromptSmem<D>::TOTAL;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], a, (const PromptList*)list, (const PromptItem*)items, pair);
+}
+
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st) {
+  if (a.act == ActKind::F16)
+    return a.head_dim == 64 ? prompt_launch<__half, 64>(a, ws, num_sms, st) : prompt_launch<__half, 128>(a, ws, num_sms, st);
+  return a.head_dim == 64 ? prompt_launch<__nv_bfloat16, 64>(a, ws, num_sms, st)
+                          : prompt_launch<__nv_bfloat16, 128>(a, ws, num_sms, st);
 }
 
 }  // namespace ds
