@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_append_kernel(const PagedAp
   constexpr int RPI = 32 / LPR;  // rows a warp holds at once
   constexpr int U = 4;           // row groups loaded together
   const int lane = threadIdx.x & 31, ch = lane % LPR;
+  pdl_wait();
+  pdl_launch_dependents();
   const long long w = ((long long)blockIdx.x * kRowThreads + threadIdx.x) >> 5;
   const int t = (int)(w / subs), sub = (int)(w % subs);
   if (t >= a.tokens) return;
@@ -202,6 +204,8 @@ template <typename ACT, int D, bool U4>
 __global__ void __launch_bounds__(kRowThreads) paged_gather_kernel(const PagedGatherArgs a, int subs, int iters) {
   constexpr int LPR = D / 8, RPI = 32 / LPR, U = 4;
   const int lane = threadIdx.x & 31, ch = lane % LPR;
+  pdl_wait();
+  pdl_launch_dependents();
   const long long w = ((long long)blockIdx.x * kRowThreads + threadIdx.x) >> 5;
   const int t = (int)(w / subs), sub = (int)(w % subs);
   if (t >= a.tokens) return;
@@ -272,6 +276,11 @@ static cudaError_t append_launch(const PagedAppendArgs& a, int num_sms, cudaStre
   cfg.gridDim = dim3((unsigned)(((long long)a.tokens * subs + kRowThreads / 32 - 1) / (kRowThreads / 32)));
   cfg.blockDim = dim3(kRowThreads);
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (a.c.u4) {
     if (a.interleaved) return cudaLaunchKernelEx(&cfg, paged_append_kernel<ACT, D, true, true>, a, subs, iters);
     return cudaLaunchKernelEx(&cfg, paged_append_kernel<ACT, D, true, false>, a, subs, iters);
@@ -296,6 +305,11 @@ static cudaError_t gather_launch(const PagedGatherArgs& a, int num_sms, cudaStre
   cfg.gridDim = dim3((unsigned)(((long long)a.tokens * subs + kRowThreads / 32 - 1) / (kRowThreads / 32)));
   cfg.blockDim = dim3(kRowThreads);
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (a.c.u4) return cudaLaunchKernelEx(&cfg, paged_gather_kernel<ACT, D, true>, a, subs, iters);
   return cudaLaunchKernelEx(&cfg, paged_gather_kernel<ACT, D, false>, a, subs, iters);
 }

@@ -149,6 +149,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
   const int per_b = a.c.kv_heads * pl.nrt;
   const uint32_t stage0 = smem_u32(sm) + (uint32_t)(warp * NST * Tile::STAGE);
 
+  pdl_wait();
+  pdl_launch_dependents();
   // ---- this CTA's share: blocks [c_lo, c_hi) of all segments' blocks
   long long chunk, c_lo, c_hi;
   {
@@ -718,6 +720,11 @@ static cudaError_t attention_launch(const PagedAttnArgs& a, const PaPlan& pl, in
   cfg.blockDim = dim3(kPaThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, pl);
 }
 

@@ -70,6 +70,7 @@ struct PromptList {
 __global__ void __launch_bounds__(1024) prompt_list_kernel(const PromptAttnArgs a, int unit, PromptList* list,
                                                            PromptItem* items, int most) {
   __shared__ int hist[1024], s_warp[32];
+  pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   hist[tid] = 0;
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();
+  pdl_launch_dependents();
 
   const int group = a.heads / a.kv_heads;
   const int hp = pair_heads ? a.heads / 2 : a.heads;  // items per list entry
@@ -552,6 +554,11 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
   const int pair = pairs_heads(a.heads, a.kv_heads);
   const int most = (int)prompt_most(a.batch, a.q_tokens);
   cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(1024);
   cfg.stream = st;
@@ -561,11 +568,6 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
   cfg.gridDim = dim3((unsigned)(ctas < num_sms ? ctas : num_sms));
   cfg.blockDim = dim3(kPrThreads);
   cfg.dynamicSmemBytes = PromptSmem<D>::TOTAL;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], a, (const PromptList*)list, (const PromptItem*)items, pair);
 }
 

@@ -415,18 +415,40 @@ def _check_like(t, shape, dtype, what):
 
 
 def _check_int32(t, numel, what):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < numel or (numel > 1 and t.stride(0) != 1):
+    """The address of an int32 vector of at least numel elements."""
+    if t.dtype is not _torch().int32 or t.dim() != 1 or t.shape[0] < numel or (numel > 1 and t.stride(0) != 1):
         raise ValueError(f"{what}: expected an int32 vector of at least {numel} elements, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _packed(t, dtype, heads, head_dim, what):
-    """Token stride in elements of a packed tensor [tokens][heads][head_dim]."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads) or \
-            t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
-        raise ValueError(f"{what}: expected a {dtype} tensor [tokens][{heads if heads is not None else 'heads'}]"
-                         f"[{head_dim}] with contiguous heads, got {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim
+    """(address, token stride in elements) of a packed tensor [tokens][heads][head_dim]."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 3 or shape[2] != head_dim or shape[1] != heads or stride[2] != 1 or \
+            (heads > 1 and stride[1] != head_dim):
+        raise ValueError(f"{what}: expected a {dtype} tensor [tokens][{heads}][{head_dim}] with contiguous heads, got "
+                         f"{t.dtype} {tuple(shape)} with strides {tuple(stride)}")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * head_dim)
+
+
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _raw_stream(s):
+    """As _stream, as an integer; the current stream without a torch.cuda.Stream object where torch can tell."""
+    if s is not None:
+        return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+    torch = _torch()
+    fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return fast(torch.cuda.current_device()) if fast is not None else torch.cuda.current_stream().cuda_stream
 
 
 def paged_cache(k, v, block_table, act_dtype, k_scale=None, v_scale=None):
@@ -451,7 +473,7 @@ def paged_cache(k, v, block_table, act_dtype, k_scale=None, v_scale=None):
                        _ptr(block_table), num_pages, page_size, block_table.shape[1], kv_heads,
                        2 * row if codes else row, DS_U4 if codes else _dtype_code(act_dtype), _dtype_code(act_dtype))
     c.tensors = (k, v, k_scale, v_scale, block_table)
-    c.torch_dtype = act_dtype
+    c.shape = (kv_heads, c.head_dim, act_dtype, block_table.shape[0])
     return c
 
 
@@ -465,40 +487,43 @@ def rotary(cos_sin, interleaved=False):
     return r
 
 
-def _check_batch(cache, batch):
-    if cache.tensors[4].shape[0] < batch:
-        raise ValueError(f"block_table: {cache.tensors[4].shape[0]} rows for a batch of {batch}")
+def _check_batch(rows, batch):
+    if rows < batch:
+        raise ValueError(f"block_table: {rows} rows for a batch of {batch}")
 
 
 def ds_paged_append(cache, q, k, v, q_out, cu_seqlens, past_len, batch, rotary, ws, stream=None):
     """q (and q_out) and rotary may be None; a workspace tensor of 256 bytes or more."""
-    tokens, nk, d, dt = k.shape[0], cache.kv_heads, cache.head_dim, cache.torch_dtype
-    ks, vs = _packed(k, dt, nk, d, "k"), _packed(v, dt, nk, d, "v")
+    nk, d, dt, rows = cache.shape
+    tokens = k.shape[0]
+    kp, ks = _packed(k, dt, nk, d, "k")
+    vp, vs = _packed(v, dt, nk, d, "v")
     heads = qs = qos = 0
+    qp = qop = None
     if q is not None:
         heads = q.shape[1]
-        qs, qos = _packed(q, dt, heads, d, "q"), _packed(q_out, dt, heads, d, "q_out")
+        qp, qs = _packed(q, dt, heads, d, "q")
+        qop, qos = _packed(q_out, dt, heads, d, "q_out")
     if v.shape[0] != tokens or (q is not None and not q.shape[0] == q_out.shape[0] == tokens):
         raise ValueError("q, k, v and q_out must have the same number of tokens")
-    _check_int32(cu_seqlens, batch + 1, "cu_seqlens")
-    _check_int32(past_len, batch, "past_len")
-    _check_batch(cache, batch)
-    _check(load().ds_paged_append(C.byref(cache), C.byref(rotary) if rotary is not None else None, _ptr(q),
-                                  _ptr(q_out) if q is not None else None, heads, _ptr(k), _ptr(v), qs, qos, ks, vs,
-                                  tokens, _ptr(cu_seqlens), _ptr(past_len), batch, _ptr(ws), ws.numel(),
-                                  _stream(stream)), "ds_paged_append")
+    cu, past = _check_int32(cu_seqlens, batch + 1, "cu_seqlens"), _check_int32(past_len, batch, "past_len")
+    _check_batch(rows, batch)
+    _check(load().ds_paged_append(C.byref(cache), C.byref(rotary) if rotary is not None else None, qp, qop, heads, kp, vp,
+                                  qs, qos, ks, vs, tokens, cu, past, batch, ws.data_ptr(), ws.numel(),
+                                  _raw_stream(stream)), "ds_paged_append")
 
 
 def ds_paged_gather(cache, k_out, v_out, cu_seqlens, first_pos, batch, ws, stream=None):
-    tokens, nk, d, dt = k_out.shape[0], cache.kv_heads, cache.head_dim, cache.torch_dtype
-    ks, vs = _packed(k_out, dt, nk, d, "k_out"), _packed(v_out, dt, nk, d, "v_out")
+    nk, d, dt, rows = cache.shape
+    tokens = k_out.shape[0]
+    kp, ks = _packed(k_out, dt, nk, d, "k_out")
+    vp, vs = _packed(v_out, dt, nk, d, "v_out")
     if v_out.shape[0] != tokens:
         raise ValueError("k_out and v_out must have the same number of tokens")
-    _check_int32(cu_seqlens, batch + 1, "cu_seqlens")
-    _check_int32(first_pos, batch, "first_pos")
-    _check_batch(cache, batch)
-    _check(load().ds_paged_gather(C.byref(cache), _ptr(k_out), _ptr(v_out), ks, vs, tokens, _ptr(cu_seqlens),
-                                  _ptr(first_pos), batch, _ptr(ws), ws.numel(), _stream(stream)), "ds_paged_gather")
+    cu, first = _check_int32(cu_seqlens, batch + 1, "cu_seqlens"), _check_int32(first_pos, batch, "first_pos")
+    _check_batch(rows, batch)
+    _check(load().ds_paged_gather(C.byref(cache), kp, vp, ks, vs, tokens, cu, first, batch, ws.data_ptr(), ws.numel(),
+                                  _raw_stream(stream)), "ds_paged_gather")
 
 
 def ds_paged_attention_workspace_bytes(cache, heads, batch, new_tokens):
@@ -507,15 +532,17 @@ def ds_paged_attention_workspace_bytes(cache, heads, batch, new_tokens):
 
 def ds_paged_attention(cache, q, out, past_len, batch, new_tokens, ws, ws_bytes, scale=None, stream=None):
     """scale None: 1 / sqrt(head_dim)."""
-    heads, d, dt = q.shape[1], cache.head_dim, cache.torch_dtype
-    qs, os_ = _packed(q, dt, heads, d, "q"), _packed(out, dt, heads, d, "out")
+    nk, d, dt, rows = cache.shape
+    heads = q.shape[1]
+    qp, qs = _packed(q, dt, heads, d, "q")
+    op, os_ = _packed(out, dt, heads, d, "out")
     if q.shape[0] != batch * new_tokens or out.shape[0] != q.shape[0]:
         raise ValueError("q and out must have batch * new_tokens rows")
-    _check_int32(past_len, batch, "past_len")
-    _check_batch(cache, batch)
-    _check(load().ds_paged_attention(C.byref(cache), _ptr(q), _ptr(out), heads, qs, os_, _ptr(past_len), batch,
-                                     new_tokens, scale if scale is not None else d ** -0.5, _ptr(ws), ws_bytes,
-                                     _stream(stream)), "ds_paged_attention")
+    past = _check_int32(past_len, batch, "past_len")
+    _check_batch(rows, batch)
+    _check(load().ds_paged_attention(C.byref(cache), qp, op, heads, qs, os_, past, batch, new_tokens,
+                                     scale if scale is not None else d ** -0.5, ws.data_ptr(), ws_bytes,
+                                     _raw_stream(stream)), "ds_paged_attention")
 
 
 def ds_prompt_attention_workspace_bytes(heads, batch, tokens):
@@ -526,16 +553,16 @@ def ds_prompt_attention(q, k, v, out, cu_q, cu_k, batch, ws, ws_bytes, scale=Non
     """q, out [q_tokens][heads][head_dim]; k, v [k_tokens][kv_heads][head_dim];
     scale None: 1 / sqrt(head_dim)."""
     dt, (nq, heads, d), (nk, kv_heads, _) = q.dtype, q.shape, k.shape
-    qs, ks = _packed(q, dt, heads, d, "q"), _packed(k, dt, kv_heads, d, "k")
-    vs, os_ = _packed(v, dt, kv_heads, d, "v"), _packed(out, dt, heads, d, "out")
+    qp, qs = _packed(q, dt, heads, d, "q")
+    kp, ks = _packed(k, dt, kv_heads, d, "k")
+    vp, vs = _packed(v, dt, kv_heads, d, "v")
+    op, os_ = _packed(out, dt, heads, d, "out")
     if out.shape[0] != nq or v.shape[0] != nk:
         raise ValueError("q and out, and k and v, must have the same number of tokens")
-    _check_int32(cu_q, batch + 1, "cu_q")
-    _check_int32(cu_k, batch + 1, "cu_k")
-    _check(load().ds_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(out), heads, kv_heads, d, _dtype_code(dt), qs,
-                                      ks, vs, os_, nq, nk, _ptr(cu_q), _ptr(cu_k), batch,
-                                      scale if scale is not None else d ** -0.5, _ptr(ws), ws_bytes,
-                                      _stream(stream)), "ds_prompt_attention")
+    _check(load().ds_prompt_attention(qp, kp, vp, op, heads, kv_heads, d, _dtype_code(dt), qs, ks, vs, os_, nq, nk,
+                                      _check_int32(cu_q, batch + 1, "cu_q"), _check_int32(cu_k, batch + 1, "cu_k"),
+                                      batch, scale if scale is not None else d ** -0.5, ws.data_ptr(), ws_bytes,
+                                      _raw_stream(stream)), "ds_prompt_attention")
 
 
 def ds_launch_count():
