@@ -104,9 +104,12 @@ struct RowLane {
 };
 
 // Quantises the row whose channels the LPR lanes of this lane's group hold, 16
-// each: the codes of its two chunks, and the row's (scale, minimum).  The
-// quotient is taken by the reciprocal, off by under 2^-18 of a step, and again
-// by division in the rare groups where that could decide a rounding.
+// each: the codes of its two chunks, and the row's (scale, minimum).
+// code = clamp(rne(d / s), 0, 15), d = x - m, by the reciprocal: t = d / (15 s),
+// clamped to [0, 1] by the multiplication, is off by under 2^-22, and 15 t + 1.5
+// 2^23 rounds it to an integer in the low bits.  Where t lies that near a half,
+// the exact remainder d - (k + 1/2) s decides (a product of 5 and 11 bits, one
+// rounding), and the float32 division itself where it could round to the half.
 template <int LPR>
 __device__ __forceinline__ uint2 quantize_row(const float (&x)[16], __half2* scale) {
   float lo = x[0], hi = x[0];
@@ -122,40 +125,52 @@ __device__ __forceinline__ uint2 quantize_row(const float (&x)[16], __half2* sca
   }
   const __half m = __float2half_rn(lo);
   const float mf = __half2float(m);
-  const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, mf), 15.f));
-  const float sf = __half2float(s), inv = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  // (hi - m) / 15, correctly rounded: one step from the product with the reciprocal
+  const float range = __fsub_rn(hi, mf), q15 = range * (1.f / 15.f);
+  const __half s = __float2half_rn(fmaf(fmaf(-15.f, q15, range), 1.f / 15.f, q15));
+  const float sf = __half2float(s);
+  const float inv = sf > 0.f ? __fdividef(1.f, sf * 15.f) : 0.f;
   *scale = __halves2half2(s, m);
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
+  constexpr float kMagic = 12582912.f;
+  constexpr uint32_t kMagicBits = 0x4B400000u;  // its bits: their multiples of 16 wrap to a constant
+  constexpr uint32_t kFix = kMagicBits * 0x11111111u;
   uint32_t w[2] = {0u, 0u};
-  float near = 1.f;  // smallest distance of a quotient from a half
+  float far = 0.f;  // largest distance of a quotient from its code
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float t = fminf(fmaxf(__fsub_rn(x[i], mf) * inv, 0.f), 15.f);
-    const float u = __fadd_rn(t, kMagic);
-    near = fminf(near, fabsf(fabsf(__fsub_rn(t, __fsub_rn(u, kMagic))) - 0.5f));
-    w[i >> 3] |= (__float_as_uint(u) & 15u) << (4 * (i & 7));
+    const float t = __saturatef(__fsub_rn(x[i], mf) * inv);
+    const float u = fmaf(t, 15.f, kMagic);
+    far = fmaxf(far, fabsf(fmaf(t, 15.f, -__fsub_rn(u, kMagic))));
+    w[i >> 3] += __float_as_uint(u) << (4 * (i & 7));
   }
-  if (near < 3.0e-5f && sf > 0.f) {
-    w[0] = w[1] = 0u;
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      float xi = x[0];
+  w[0] -= kFix;
+  w[1] -= kFix;
+  constexpr float kNear = 0.5f - 3.0e-5f;
+  if (far > kNear) {
 #pragma unroll
-      for (int k = 1; k < 16; ++k) xi = i == k ? x[k] : xi;
-      const float r = rintf(__fdiv_rn(__fsub_rn(xi, mf), sf));
-      const uint32_t code = (uint32_t)fminf(fmaxf(r, 0.f), 15.f) << (4 * (i & 7));
-      if (i < 8) w[0] |= code;
-      else w[1] |= code;
+    for (int i = 0; i < 16; ++i) {
+      const float d = __fsub_rn(x[i], mf), t = __saturatef(d * inv);
+      const float r = __fsub_rn(fmaf(t, 15.f, kMagic), kMagic);
+      const float e = fmaf(t, 15.f, -r);
+      if (fabsf(e) > kNear) {
+        const float low = e > 0.f ? r : r - 1.f;  // the code below the half
+        const float rem = fmaf(-(low + 0.5f), sf, d);
+        float c = rem > 0.f ? low + 1.f : low;
+        if (rem == 0.f) c = rintf(low + 0.5f);
+        else if (fabsf(rem) < sf * 2e-6f) c = rintf(__fdiv_rn(d, sf));
+        const int sh = 4 * (i & 7);
+        w[i >> 3] = (w[i >> 3] & ~(15u << sh)) | ((uint32_t)c << sh);
+      }
     }
   }
   return make_uint2(w[0], w[1]);
 }
 
 template <typename ACT, int D, bool U4, bool INTER>
-__global__ void __launch_bounds__(kRowThreads) paged_append_kernel(const PagedAppendArgs a, int subs, int iters) {
+__global__ void __launch_bounds__(kRowThreads, 5) paged_append_kernel(const PagedAppendArgs a, int subs, int iters) {
   constexpr int LPR = D / 16;    // lanes per row
   constexpr int RPI = 32 / LPR;  // rows a warp holds at once
-  constexpr int U = 4;           // row groups loaded together
+  constexpr int U = U4 ? 2 : 4;  // row groups loaded together
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -308,11 +323,11 @@ __global__ void __launch_bounds__(kRowThreads) paged_gather_kernel(const PagedGa
 }
 
 // Splits a token's `groups` row groups over as many warps as keep the GPU
-// busy: one warp does up to 16 groups, fewer while there are under 16 warps an
-// SM in the launch.
+// busy: one warp does up to 16 groups, fewer while there are under 48 warps an
+// SM in the launch (the look-ups' latency needs warps to hide behind).
 static void split_rows(int tokens, int groups, int num_sms, int* subs, int* iters) {
   int it = 16;
-  while (it > 1 && (long long)tokens * ((groups + it - 1) / it) < 16LL * num_sms) it >>= 1;
+  while (it > 1 && (long long)tokens * ((groups + it - 1) / it) < 48LL * num_sms) it >>= 1;
   *iters = it;
   *subs = (groups + it - 1) / it;
 }
