@@ -25,8 +25,10 @@
 //  * codes become fp16 operands by one AND: a four-bit field at bit 0 or 4 of a
 //    16-bit half is the subnormal number c 2^-24 or c 2^-20, which the tensor
 //    cores multiply exactly; the powers of two go into the scales.
-//  * running maximum per row (log2 domain), sums per lane; O is only rescaled
-//    in the steps in which a maximum rises.
+//  * scores are taken relative to a reference per row (log2 domain) that follows
+//    the maximum only when it is 2^8 behind: a step then needs one vote, no
+//    shuffles, and O is rarely rescaled (any reference gives the same quotient;
+//    weights up to 256 keep their relative rounding); sums stay per lane.
 // Copies: each warp streams its own tiles (16 to 64 positions) through a ring of
 // three or four stages with cp.async, 16-byte chunks XOR-swizzled; rows past the
 // sequence are zero-filled without being read.  A tile's 16-position blocks lie
@@ -48,11 +50,45 @@ namespace ds {
 
 constexpr int kPaWarps = 4;
 constexpr int kPaThreads = kPaWarps * 32;
-constexpr int kPaCtasPerSm = 2;
+// CTAs per SM: 4-bit pages need more warps to hide the unpacking's latency; their
+// tiles are small enough for three (and the registers, with up to 8 rows).
+__host__ __device__ constexpr int pa_ctas(bool u4, int nr) { return u4 && nr == 1 ? 3 : 2; }
 
-__device__ __forceinline__ void pa_cp16(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void pa_cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void pa_cp16_or_zero(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+// Two fp32 lanes of one instruction.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+constexpr float kPaBehind = 8.f;  // log2 that a row's scores may be ahead of its reference
 __device__ __forceinline__ void pa_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void pa_wait() {
@@ -94,7 +130,7 @@ struct PaTile {
   static constexpr int ROW = U4 ? D / 2 : D * 2;  // bytes of a row
   static constexpr int BLOCK = 2 * 16 * ROW + (U4 ? 128 : 0);
   static constexpr int STAGE = KB * BLOCK;
-  static constexpr int NST = U4 && D == 64 ? 4 : 3;
+  static constexpr int NST = U4 ? (D == 128 ? 2 : 4) : 3;
   static constexpr int SMEM = kPaWarps * NST * STAGE;
   // Byte offset of 16-byte chunk c of row r among a block's rows: ldmatrix reads
   // 8 rows at one chunk, the code loads 4 rows at 16 or 32 bytes.
@@ -129,7 +165,7 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
 __device__ __forceinline__ int pa_blocks(const PagedAttnArgs& a, int b) { return max(1, (pa_len(a, b) + 15) >> 4); }
 
 template <typename ACT, int D, bool U4, int NR>
-__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
+__global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
     paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ PaPlan pl) {
   using Tile = PaTile<D, U4>;
   constexpr int KB = Tile::KB, NST = Tile::NST, ROW = Tile::ROW;
@@ -212,45 +248,67 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
     // page of block j of tile ti (lane j < KB), -1: none
     auto tile_page = [&](int ti) {
       const int blk = k0 + ti * KB + lane;
-      if (lane >= KB || ti >= ntile || blk >= k1 || blk * 16 >= len) return -1;
-      const int p = table[(blk * 16) >> a.c.page_shift];
-      if (p < 0 || p >= a.c.num_pages) {
-        bad |= kFlagBadPage;
-        return -1;
+      int p = -1;
+      if (lane < KB && blk < min(k1, (len + 15) >> 4)) {
+        p = table[(blk * 16) >> a.c.page_shift];
+        if (p < 0 || p >= a.c.num_pages) {
+          bad |= kFlagBadPage;
+          p = -1;
+        }
       }
       return p;
     };
+    // this lane's 16 bytes of row 0 of the head's first page
+    const char* kl = static_cast<const char*>(a.c.k) + ((size_t)kh << a.c.page_shift) * ROW + lane * 16;
+    const char* vl = static_cast<const char*>(a.c.v) + ((size_t)kh << a.c.page_shift) * ROW + lane * 16;
+    const uint32_t page_rows = (uint32_t)a.c.kv_heads << a.c.page_shift;  // (65535 heads of 128 rows at most)
     auto issue = [&](int ti, int page, int slot) {
-      holes &= ~(((1u << KB) - 1u) << (slot * KB));
-      holes |= (~__ballot_sync(0xffffffffu, page >= 0) & ((1u << KB) - 1u)) << (slot * KB);
+      const unsigned some = __ballot_sync(0xffffffffu, page >= 0) & ((1u << KB) - 1u);
+      holes = (holes & ~(((1u << KB) - 1u) << (slot * KB))) | ((~some & ((1u << KB) - 1u)) << (slot * KB));
       if (ti < ntile) {
+        const int pos_t = (k0 + ti * KB) * 16;
+        const uint32_t dst_t = stage0 + (uint32_t)(slot * Tile::STAGE);
+        constexpr int CPR = ROW / 16;   // chunks per row
+        constexpr int RPP = 32 / CPR;   // rows a warp copies at once
+        const int r0 = lane / CPR, c0 = lane % CPR;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
           const int pg = __shfl_sync(0xffffffffu, page, j);
-          const int pos = (k0 + ti * KB + j) * 16;
-          const int n = pg < 0 ? 0 : min(16, len - pos);  // rows that exist
-          const long long row = pg < 0 ? 0
-                                       : (((long long)pg * a.c.kv_heads + kh) << a.c.page_shift) +
-                                             (pos & ((1 << a.c.page_shift) - 1));
-          const uint32_t dst = stage0 + (uint32_t)(slot * Tile::STAGE + j * Tile::BLOCK);
-          const char* ksrc = static_cast<const char*>(a.c.k) + row * ROW;
-          const char* vsrc = static_cast<const char*>(a.c.v) + row * ROW;
-          constexpr int CPR = ROW / 16;  // chunks per row
+          const int pos = pos_t + j * 16;
+          const uint32_t dst = dst_t + (uint32_t)(j * Tile::BLOCK);
+          const uint32_t in_page = (uint32_t)pos & ((1u << a.c.page_shift) - 1u);
+          const size_t at = ((size_t)(uint32_t)pg * page_rows + in_page) * ROW;
+          if (pg >= 0 && pos + 16 <= len) {
+            const char *ks = kl + at, *vs = vl + at;
 #pragma unroll
-          for (int i = lane; i < 16 * CPR; i += 32) {
-            const int r = i / CPR, c = i % CPR;
-            const uint32_t o = Tile::off(r, c);
-            const size_t so = r < n ? (size_t)i * 16 : 0;
-            pa_cp16(dst + o, ksrc + so, r < n);
-            pa_cp16(dst + 16 * ROW + o, vsrc + so, r < n);
-          }
-          if constexpr (U4) {
-            if (lane < 8) {  // 16 (scale, minimum) pairs of K, then of V: zeros where no row of the chunk exists
-              const int c = lane & 3;
-              const char* s = static_cast<const char*>(lane < 4 ? a.c.k_scale : a.c.v_scale) + row * 4;
-              const bool ok = 4 * c < n;
-              pa_cp16(dst + 32 * ROW + lane * 16, s + (ok ? c * 16 : 0), ok);
+            for (int i = 0; i < 16 / RPP; ++i) {
+              const uint32_t o = dst + Tile::off(r0 + i * RPP, c0);
+              pa_cp16(o, ks + i * 512);
+              pa_cp16(o + 16 * ROW, vs + i * 512);
             }
+          } else {  // rows behind the sequence (or the whole block) are zeros
+            const int n = pg < 0 ? 0 : len - pos;
+#pragma unroll
+            for (int i = 0; i < 16 / RPP; ++i) {
+              const int r = r0 + i * RPP;
+              const uint32_t o = dst + Tile::off(r, c0);
+              const size_t so = r < n ? at + i * 512 : 0;
+              pa_cp16_or_zero(o, kl + so, r < n);
+              pa_cp16_or_zero(o + 16 * ROW, vl + so, r < n);
+            }
+          }
+        }
+        if constexpr (U4) {
+          // 16 (scale, minimum) pairs of K, then of V, of every block, eight lanes a
+          // block: zeros where no row of the 16-byte chunk exists
+          const int j = lane >> 3, c = lane & 3, pos = pos_t + j * 16;
+          const int pg = __shfl_sync(0xffffffffu, page, j & (KB - 1));
+          if (j < KB) {
+            const uint32_t in_page = (uint32_t)pos & ((1u << a.c.page_shift) - 1u);
+            const bool ok = pg >= 0 && pos + 4 * c < len;
+            const size_t row = ok ? (size_t)(uint32_t)pg * page_rows + ((uint32_t)kh << a.c.page_shift) + in_page + 4 * c : 0;
+            const char* sp = static_cast<const char*>((lane & 4) ? a.c.v_scale : a.c.k_scale) + row * 4;
+            pa_cp16_or_zero(dst_t + (uint32_t)(j * Tile::BLOCK) + 32 * ROW + (lane & 7) * 16, sp, ok);
           }
         }
       }
@@ -341,7 +399,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
       m[nr][0] = m[nr][1] = -INFINITY;
       l[nr][0] = l[nr][1] = om[nr][0] = om[nr][1] = 0.f;
     }
-    int ve = -14;  // 4-bit: exponent that the weights' scales are held relative to
+    int ve = -14;  // 4-bit: the weights' scales are held relative to 2^ve
+    float vmul = 16384.f;
 
     int slot = 0;
     for (int ti = warp; ti < ntile; ti += kPaWarps) {
@@ -393,99 +452,117 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
             }
         }
       }
-      // ---- scores in the log2 domain, mask, running maximum
+      // ---- scores in the log2 domain relative to the row's reference, mask
       const int pos0 = (k0 + ti * KB) * 16;
-      float2 vsm[KB][2];  // 4-bit: (scale, minimum) of the lane's two value rows per block
-      const bool tail = hole != 0 || pos0 + KB * 16 > past + 1;  // some row may not see all of the tile
-      float mx[NR][2];
+      uint32_t vsm[KB][2];  // 4-bit: (scale, minimum) of the lane's two value rows per block
+      F2 ref[NR];
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
+      for (int nr = 0; nr < NR; ++nr)
+        ref[nr] = F2{m[nr][0] == -INFINITY ? 0.f : -m[nr][0], m[nr][1] == -INFINITY ? 0.f : -m[nr][1]};
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
-        const uint32_t sc = st + (uint32_t)(j * Tile::BLOCK) + 32 * ROW;
-        float2 ksm[2];
-        int key[2] = {g, g + 8};
         if constexpr (U4) {
-          key[0] = Tile::key(g);
-          key[1] = Tile::key(g + 8);
+          const uint32_t sc = st + (uint32_t)(j * Tile::BLOCK) + 32 * ROW;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t u;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(sc + key[i] * 4) : "memory");
-            ksm[i] = __half22float2(*reinterpret_cast<__half2*>(&u));
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(sc + 64 + key[i] * 4) : "memory");
-            vsm[j][i] = __half22float2(*reinterpret_cast<__half2*>(&u));
+            const uint32_t at = sc + Tile::key(g + 8 * i) * 4;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vsm[j][i]) : "r"(at + 64) : "memory");
+            const float2 ks = __half22float2(*reinterpret_cast<__half2*>(&u));
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              const F2 t = mul2(F2{q_mul[nr][0], q_mul[nr][1]}, F2{ks.x, ks.x});
+              const F2 z = fma2(F2{q_sum[nr][0], q_sum[nr][1]}, F2{ks.y, ks.y}, ref[nr]);
+              const F2 y = fma2(F2{s[j][nr][2 * i], s[j][nr][2 * i + 1]}, t, z);
+              s[j][nr][2 * i] = y.x;
+              s[j][nr][2 * i + 1] = y.y;
+            }
           }
-        }
+        } else {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+          for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float& x = s[j][nr][i];
-            if constexpr (U4) x = fmaf(x * ksm[i >> 1].x, q_mul[nr][i & 1], ksm[i >> 1].y * q_sum[nr][i & 1]);
-            else x *= q_mul[nr][i & 1];
-            if (tail && (((hole >> j) & 1u) != 0 || pos0 + j * 16 + key[i >> 1] > lim[nr][i & 1])) x = -INFINITY;
-          }
-        if (tail && U4) {  // rows behind the sequence share a 16-byte chunk with its last scales
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (pos0 + j * 16 + key[i] >= len) vsm[j][i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < 2; ++i) {
+              const F2 y = fma2(F2{s[j][nr][2 * i], s[j][nr][2 * i + 1]}, F2{q_mul[nr][0], q_mul[nr][1]}, ref[nr]);
+              s[j][nr][2 * i] = y.x;
+              s[j][nr][2 * i + 1] = y.y;
+            }
         }
       }
-#pragma unroll
-      for (int j = 0; j < KB; ++j)
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx[nr][i & 1] = fmaxf(mx[nr][i & 1], s[j][nr][i]);
-      float rise = 0.f;
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x = mx[nr][i];
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          mx[nr][i] = fmaxf(m[nr][i], x);
-          if (mx[nr][i] != m[nr][i]) rise = 1.f;
-        }
-      float vf = 1.f, vmul = 1.f;
-      if constexpr (U4) {
-        // the largest scale of the tile, to a power of two: weights times scales then
-        // stay within fp16 whatever the values' size
-        unsigned top = 0;
+      if (hole != 0 || pos0 + KB * 16 > past + 1) {  // some row may not see all of the tile, or rows are missing
 #pragma unroll
         for (int j = 0; j < KB; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) top = max(top, __float_as_uint(fabsf(vsm[j][i].x)));
-        top = __reduce_max_sync(0xffffffffu, top);
-        const int e = min((int)(top >> 23) - 127, 16);
-        if (e > ve) {
-          vf = exp2f((float)(ve - e));
-          ve = e;
-          rise = 1.f;
-        }
-        vmul = exp2f((float)-ve);
+          for (int i = 0; i < 4; ++i) {
+            const int key = U4 ? Tile::key(g + 8 * (i >> 1)) : g + 8 * (i >> 1);
+            const int pos = pos0 + j * 16 + key;
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+              if (((hole >> j) & 1u) != 0 || pos > lim[nr][i & 1]) s[j][nr][i] = -INFINITY;
+            // (rows behind the sequence share a 16-byte chunk with its last scales)
+            if (U4 && (i & 1) == 0 && pos >= len) vsm[j][i >> 1] = 0u;
+          }
       }
-      if (__any_sync(0xffffffffu, rise != 0.f)) {
+      // ---- the reference follows where a score is far ahead of it (or there is none yet)
+      float mx[NR][2];
+      bool rise = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        mx[nr][0] = mx[nr][1] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) mx[nr][i] = fmaxf(mx[nr][i], fmaxf(s[j][nr][i], s[j][nr][i + 2]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          rise = rise || mx[nr][i] > kPaBehind || (m[nr][i] == -INFINITY && mx[nr][i] > -INFINITY);
+      }
+      if constexpr (U4) {
+        // the largest scale so far, as a power of two: weights times scales then stay
+        // within fp16 whatever the values' size
+        unsigned vtop = 0;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) vtop = max(vtop, max(vsm[j][0] & 0x7fffu, vsm[j][1] & 0x7fffu));
+        vtop = __reduce_max_sync(0xffffffffu, vtop);
+        const int e = (int)(vtop >> 10) - 15;
+        if (e > ve) {
+          const float vf = exp2f((float)(ve - e));
+          ve = e;
+          vmul = exp2f((float)-ve);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[mt][nr][i] *= vf;
+        }
+      }
+      if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          float al[2];
+          float al[2], down[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            al[i] = mx[nr][i] == -INFINITY ? 1.f : ex2(m[nr][i] - mx[nr][i]);
-            m[nr][i] = mx[nr][i];
+            float x = mx[nr][i];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float old = m[nr][i] == -INFINITY ? 0.f : m[nr][i];
+            const float now = m[nr][i] == -INFINITY ? x : fmaxf(m[nr][i], m[nr][i] + x);
+            al[i] = now == -INFINITY ? 1.f : ex2(m[nr][i] - now);
+            down[i] = now == -INFINITY ? 0.f : now - old;
+            m[nr][i] = now;
             l[nr][i] *= al[i];
             om[nr][i] *= al[i];
-            al[i] *= vf;
           }
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            o[mt][nr][0] *= al[0];
-            o[mt][nr][1] *= al[1];
-            o[mt][nr][2] *= al[0];
-            o[mt][nr][3] *= al[1];
-          }
+          for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][nr][i] -= down[i & 1];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][nr][i] *= al[i & 1];
         }
       }
       // ---- weights, and O^T += V^T P^T
@@ -495,19 +572,22 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
         uint32_t pf[NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          float p[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float mm = m[nr][i & 1] == -INFINITY ? 0.f : m[nr][i & 1];
-            p[i] = ex2(s[j][nr][i] - mm);
-            l[nr][i & 1] += p[i];
+          for (int i = 0; i < 2; ++i) {  // positions g and g + 8 (4-bit: those of operand rows g, g + 8)
+            F2 p{ex2(s[j][nr][2 * i]), ex2(s[j][nr][2 * i + 1])};
+            const F2 sum = add2(F2{l[nr][0], l[nr][1]}, p);
+            l[nr][0] = sum.x;
+            l[nr][1] = sum.y;
             if constexpr (U4) {
-              om[nr][i & 1] = fmaf(p[i], vsm[j][i >> 1].y, om[nr][i & 1]);
-              p[i] *= vsm[j][i >> 1].x * vmul;
+              const float2 vs = __half22float2(*reinterpret_cast<__half2*>(&vsm[j][i]));
+              const F2 mins = fma2(p, F2{vs.y, vs.y}, F2{om[nr][0], om[nr][1]});
+              om[nr][0] = mins.x;
+              om[nr][1] = mins.y;
+              const float f = vs.x * vmul;
+              p = mul2(p, F2{f, f});
             }
+            pf[nr][i] = transpose8x8(Act<OP>::pack2(p.x, p.y));
           }
-          pf[nr][0] = transpose8x8(Act<OP>::pack2(p[0], p[1]));
-          pf[nr][1] = transpose8x8(Act<OP>::pack2(p[2], p[3]));
         }
         if constexpr (!U4) {
 #pragma unroll
@@ -635,18 +715,28 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
           const int r = i / (D / 4), c = (i % (D / 4)) * 4;
           float M = -INFINITY, L = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = first; k <= last; ++k) {
-            const size_t at = ((size_t)k * 2 + (k == first ? 1 : 0)) * RP + r;
-            const float mk = ld_cg(pl.part_ml + at * 2), lk = ld_cg(pl.part_ml + at * 2 + 1);
-            const float4 x = ld_cg4(pl.part_o + at * D + c);
-            if (mk == -INFINITY && lk == 0.f) continue;
-            const float mn = fmaxf(M, mk), f0 = ex2(M - mn), f1 = ex2(mk - mn);
-            L = L * f0 + lk * f1;
-            v.x = v.x * f0 + x.x * f1;
-            v.y = v.y * f0 + x.y * f1;
-            v.z = v.z * f0 + x.z * f1;
-            v.w = v.w * f0 + x.w * f1;
-            M = mn;
+          for (int k0 = first; k0 <= last; k0 += 4) {
+            float mk[4], lk[4];
+            float4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // four parts' loads on their way together
+              const int k = min(k0 + i, last);
+              const size_t at = ((size_t)k * 2 + (k == first ? 1 : 0)) * RP + r;
+              mk[i] = ld_cg(pl.part_ml + at * 2);
+              lk[i] = ld_cg(pl.part_ml + at * 2 + 1);
+              x[i] = ld_cg4(pl.part_o + at * D + c);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (k0 + i > last || (mk[i] == -INFINITY && lk[i] == 0.f)) continue;
+              const float mn = fmaxf(M, mk[i]), f0 = ex2(M - mn), f1 = ex2(mk[i] - mn);
+              L = L * f0 + lk[i] * f1;
+              v.x = v.x * f0 + x[i].x * f1;
+              v.y = v.y * f0 + x[i].y * f1;
+              v.z = v.z * f0 + x[i].z * f1;
+              v.w = v.w * f0 + x[i].w * f1;
+              M = mn;
+            }
           }
           const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
           store(r, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -672,10 +762,13 @@ struct PaWs {
   size_t counters, part_o, part_ml, total;
   int nr, nrt, grid, min_chunk;
 };
-// Blocks of 16 positions a CTA takes at least: one tile a warp.
+// Blocks of 16 positions a CTA takes at least: one 64-position tile a warp of
+// 4-bit pages; two of the smaller tiles of 16-bit ones (one sequence of 545
+// positions, 32 heads: 11.7 us against 13.0 with one, joining more parts, and
+// 11.9 with three).
 static int pa_min_chunk(const PagedView& c) {
   if (c.u4) return kPaWarps * (c.head_dim == 64 ? PaTile<64, true>::KB : PaTile<128, true>::KB);
-  return kPaWarps * (c.head_dim == 64 ? PaTile<64, false>::KB : PaTile<128, false>::KB);
+  return 2 * kPaWarps * (c.head_dim == 64 ? PaTile<64, false>::KB : PaTile<128, false>::KB);
 }
 static PaWs pa_ws(const PagedView& c, int heads, int batch, int T, int num_sms) {
   PaWs w;
@@ -687,7 +780,8 @@ static PaWs pa_ws(const PagedView& c, int heads, int batch, int T, int num_sms) 
   w.min_chunk = pa_min_chunk(c);
   const long long most = (((long long)c.table_stride << c.page_shift) / 16) * batch * c.kv_heads * w.nrt;
   const long long ctas = (most + w.min_chunk - 1) / w.min_chunk;
-  w.grid = (int)(ctas < (long long)num_sms * kPaCtasPerSm ? ctas : (long long)num_sms * kPaCtasPerSm);
+  const long long room = (long long)num_sms * pa_ctas(c.u4, w.nr);
+  w.grid = (int)(ctas < room ? ctas : room);
   const size_t slots = (size_t)w.grid * 2 * 8 * w.nr;
   w.counters = 256;
   w.part_ml = w.counters + up((size_t)batch * c.kv_heads * w.nrt * 4);
