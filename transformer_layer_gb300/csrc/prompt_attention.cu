@@ -49,7 +49,6 @@ constexpr int kPrLoadWarp = 8;   // after the softmax warps: 0-3 of tile 0, 4-7 
 constexpr int kPrMmaWarp = 9;    // and 10
 constexpr int kPrThreads = 11 * 32;
 constexpr int kPrRows = 128;     // queries per tile, keys per block
-constexpr float kPrBehind = 8.f; // log2 a row's maximum may be ahead of its reference
 
 // One entry of the work list: a tile (or two neighbouring ones) of a sequence.
 struct PromptItem {
@@ -157,6 +156,39 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b) {
       : "f"(b));
 }
 
+// Lane 0's value, known to the compiler as the same for the whole warp: loops and
+// addresses built on it stay in uniform registers (a tcgen05.mma whose operands
+// have to be moved there costs its warp ~120 cycles instead of ~60).
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// The lane of the converged warp that issues, as 0 or 1.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
+  return r;
+}
+// umma_f16 / umma_f16_tmem_a / umma_commit / mbar_arrive of the lanes with lead != 0.
+__device__ __forceinline__ void lead_umma(uint32_t lead, uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                          uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void lead_umma_tmem_a(uint32_t lead, uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc,
+                                                 uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(ta), "l"(db), "r"(idesc), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void lead_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
 // B operand with N contiguous (V as [keys][d]: rows of 128 bytes are 64 values of
 // d, 8 keys a 1024-byte group, the next 64 values of d `lead` bytes on).
 __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t lead) {
@@ -167,10 +199,11 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t 
 template <int D>
 struct PromptSmem {
   static constexpr int TILE = kPrRows * D * 2;  // bytes of a tile of Q, K or V
-  static constexpr int NST = D == 128 ? 5 : 8;  // ring stages
+  static constexpr int NST = D == 128 ? 4 : 8;  // ring stages
   static constexpr int Q = 0;
   static constexpr int RING = 2 * TILE;
-  static constexpr int BARS = RING + NST * TILE;
+  static constexpr int OUT = RING + NST * TILE;  // per softmax warp 32 rows x 128 bytes of output
+  static constexpr int BARS = OUT + 8 * 4096;
   static constexpr int TOTAL = BARS + 256 + 1024;  // and the alignment of the base
 };
 
@@ -193,7 +226,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   extern __shared__ unsigned char raw[];
   __shared__ uint32_t s_tmem;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t bars = base + SM::BARS;
   auto full = [&](int i) { return bars + 8u * i; };
   auto empty = [&](int i) { return bars + 8u * (NST + i); };
@@ -229,7 +262,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
   const int group = a.heads / a.kv_heads;
   const int hp = pair_heads ? a.heads / 2 : a.heads;  // items per list entry
-  const long long n_items = (long long)list->count * hp;
+  const long long n_items = (long long)uni(list->count) * hp;
   bool dead = false;  // a wait of this warp gave up: nothing more is waited for or issued
 
   // What an item means for tile t.
@@ -322,8 +355,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   } else if (warp == kPrMmaWarp || warp == kPrMmaWarp + 1) {
     // ------------------------------------------------------------ products
     const int t = warp - kPrMmaWarp;
+    const uint32_t lead = elect_one();
     const uint32_t idesc_s = umma_idesc(kBf16, kPrRows), idesc_o = umma_idesc(kBf16, D) | (1u << 16);
-    const uint32_t ts = tmem + (uint32_t)(t * kPrRows), to = tmem + (uint32_t)(2 * kPrRows + t * kPrRows);
+    const uint32_t tm = (uint32_t)uni((int)tmem);
+    const uint32_t ts = tm + (uint32_t)(t * kPrRows), to = tm + (uint32_t)(2 * kPrRows + t * kPrRows);
+    const uint64_t dq = umma_desc_sw128(base + SM::Q + t * TILE);
     int st = 0;
     uint32_t ph = 0, qph = 0, pph = 0;
     auto next_stage = [&]() {
@@ -332,42 +368,41 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         ph ^= 1;
       }
     };
-    auto take = [&]() {  // the ring's next stage is full
-      if (!dead) dead = !mbar_wait(full(st), ph, a.status);
-      dead = __any_sync(0xffffffffu, dead);
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar, parity, a.status));
     };
     for (int k = 0;; ++k) {
       const long long i = prompt_item(k, n_items);
       if (i < 0) break;
       const PromptItem it = items[i / hp];
       const Tile tl = tile_of(it, (int)(i % hp), t), tr = tile_of(it, (int)(i % hp), 1 - t);
-      const int n = tl.n, nkv = max(n, tr.n);
+      const int n = uni(tl.n), nkv = max(n, uni(tr.n));
+      const int lk = uni(it.lk);
       if (nkv == 0) continue;
-      if (!dead) dead = !mbar_wait(q_full(t), qph, a.status);
+      wait(q_full(t), qph);
       qph ^= 1;
-      const uint64_t dq = umma_desc_sw128(base + SM::Q + t * TILE);
       auto product_s = [&](int j) {  // S = Q K_j^T from the ring's stage; releases it
-        take();
-        if (lane == 0 && !dead) {
+        wait(full(st), ph);
+        if (!dead) {
           tc_fence_after();
           const uint64_t dk = umma_desc_sw128(base + SM::RING + st * TILE);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t step = (uint64_t)(((kk >> 2) * (kPrRows * 128) + (kk & 3) * 32) >> 4);
-            umma_f16(ts, dq + step, dk + step, idesc_s, kk > 0);
+            lead_umma(lead, ts, dq + step, dk + step, idesc_s, kk > 0);
           }
-          umma_commit(s_full(t));
-          umma_commit(empty(st));
-          if (j == n - 1) umma_commit(q_empty(t));
+          lead_commit(lead, s_full(t));
+          lead_commit(lead, empty(st));
+          if (j == n - 1) lead_commit(lead, q_empty(t));
         }
         next_stage();
       };
       auto pass = [&]() {  // a stage that only the other tile uses
-        take();
-        if (lane == 0 && !dead) mbar_arrive(empty(st));
+        wait(full(st), ph);
+        if (lead && !dead) mbar_arrive(empty(st));
         next_stage();
       };
-      if (n == 0 && lane == 0 && !dead) mbar_arrive(q_empty(t));
+      if (n == 0 && lead && !dead) mbar_arrive(q_empty(t));
       if (n > 0) product_s(0);
       else pass();
       for (int j = 0; j < nkv; ++j) {
@@ -376,26 +411,26 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           if (j + 1 < nkv) pass();
           continue;
         }
-        take();  // V_j
-        if (!dead) dead = !mbar_wait(p_full(t), pph, a.status);
-        dead = __any_sync(0xffffffffu, dead);
+        wait(full(st), ph);  // V_j
+        wait(p_full(t), pph);
         pph ^= 1;
-        if (lane == 0 && !dead) {
+        if (!dead) {
           tc_fence_after();
-          if (it.lk - j * kPrRows < kPrRows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (lk - j * kPrRows < kPrRows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           const uint64_t dv = umma_desc_mn_sw128(base + SM::RING + st * TILE, kPrRows * 128);
 #pragma unroll
           for (int kk = 0; kk < kPrRows / 16; ++kk)
-            umma_f16_tmem_a(to, ts + (uint32_t)(kk * 8), dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (j > 0 || kk > 0));
-          if (j == n - 1) umma_commit(o_full(t));
-          umma_commit(empty(st));
+            lead_umma_tmem_a(lead, to, ts + (uint32_t)(kk * 8), dv + (uint64_t)((kk * 2048) >> 4), idesc_o,
+                             (j > 0 || kk > 0));
+          if (j == n - 1) lead_commit(lead, o_full(t));
+          lead_commit(lead, empty(st));
         }
         next_stage();
         if (j + 1 < n) product_s(j + 1);
         else if (j + 1 < nkv) pass();
       }
     }
-    if (lane == 0) umma_commit(done(t));
+    lead_commit(lead, done(t));
     mbar_wait(done(t), 0, a.status);
   } else {
     // ------------------------------------------------------------ softmax
@@ -419,62 +454,85 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         sph ^= 1;
         if (dead) continue;
         tc_fence_after();
-        float s[kPrRows];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32_nowait(ts + (uint32_t)(32 * q), s + 32 * q);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_wait_ld32(s + 32 * q);
         // some row of the tile sees less than the whole block
-        if (min(it.lk - 1, tl.lim) < (j + 1) * kPrRows - 1) {
-          const int last = lim - j * kPrRows;
+        const bool masked = min(it.lk - 1, tl.lim) < (j + 1) * kPrRows - 1;
+        const int last = lim - j * kPrRows;
+        auto mask = [&](float* v, int q) {
+          if (masked) {
 #pragma unroll
-          for (int x = 0; x < kPrRows; ++x)
-            if (x > last) s[x] = -INFINITY;
-        }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(s[q], s[q + 4]);
-#pragma unroll
-        for (int x = 8; x < kPrRows; x += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], fmaxf(s[x + q], s[x + q + 4]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (__any_sync(0xffffffffu, (top - m) * c > kPrBehind)) {
-          const float mn = fmaxf(m, top);
-          const float al = mn == -INFINITY ? 1.f : pr_ex2((m - mn) * c);
-          m = mn;
-          l *= al;
-          if (j > 0) {
+            for (int x = 0; x < 32; ++x)
+              if (32 * q + x > last) v[x] = -INFINITY;
+          }
+        };
+        uint32_t p[kPrRows / 2];
+        float l0, l1, l2, l3;
+        // The weights are computed relative to the reference as it is; only where one
+        // comes out above 2^8 (or there is no reference yet) does the true maximum
+        // of the rows matter: it is taken, l and O are rescaled, and the weights are
+        // computed again.  S stays in tensor memory until then.
+        for (bool renew = j == 0;;) {
+          if (renew) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              float o[32];
-              tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
-              tmem_wait_ld32(o);
+            for (int q = 0; q < 4; ++q) {
+              float v[32];
+              tmem_ld32_nowait(ts + (uint32_t)(32 * q), v);
+              tmem_wait_ld32(v);
+              mask(v, q);
 #pragma unroll
-              for (int x = 0; x < 32; x += 2) mul2(o[x], o[x + 1], al);
-              tmem_st32(to + (uint32_t)(32 * q), reinterpret_cast<uint32_t(&)[32]>(o));
+              for (int x = 0; x < 32; x += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], fmaxf(v[x + y], v[x + y + 4]));
+            }
+            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            const float al = mn == -INFINITY ? 1.f : pr_ex2((m - mn) * c);
+            m = mn;
+            l *= al;
+            if (j > 0) {
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) mul2(o[x], o[x + 1], al);
+                tmem_st32(to + (uint32_t)(32 * q), reinterpret_cast<uint32_t(&)[32]>(o));
+              }
             }
           }
-        }
-        const float mc = m == -INFINITY ? 0.f : -m * c;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+          const float mc = m == -INFINITY ? 0.f : -m * c;
+          l0 = l1 = l2 = l3 = 0.f;
+          uint32_t top = 0;  // largest weight of each half, as 16-bit patterns (weights are positive)
+          float v[2][32];
+          tmem_ld32_nowait(ts, v[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
+          for (int q = 0; q < 4; ++q) {
+            float* w = v[q & 1];
+            tmem_wait_ld32(w);
+            if (q < 3) tmem_ld32_nowait(ts + (uint32_t)(32 * (q + 1)), v[(q + 1) & 1]);
+            mask(w, q);
 #pragma unroll
-          for (int x = 0; x < 64; x += 4) {
-            float* v = s + 64 * h + x;
-            fma2(v[0], v[1], c, mc);
-            fma2(v[2], v[3], c, mc);
+            for (int x = 0; x < 32; x += 4) {
+              fma2(w[x], w[x + 1], c, mc);
+              fma2(w[x + 2], w[x + 3], c, mc);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) v[y] = pr_ex2(v[y]);
-            add2(l0, l1, v[0], v[1]);
-            add2(l2, l3, v[2], v[3]);
-            p[x / 2] = Act<ACT>::pack2(v[0], v[1]);
-            p[x / 2 + 1] = Act<ACT>::pack2(v[2], v[3]);
+              for (int y = 0; y < 4; ++y) w[x + y] = pr_ex2(w[x + y]);
+              add2(l0, l1, w[x], w[x + 1]);
+              add2(l2, l3, w[x + 2], w[x + 3]);
+              const int at = 16 * q + x / 2;
+              p[at] = Act<ACT>::pack2(w[x], w[x + 1]);
+              p[at + 1] = Act<ACT>::pack2(w[x + 2], w[x + 3]);
+              top = __vimax3_s16x2(top, p[at], p[at + 1]);
+            }
           }
-          tmem_st32(ts + (uint32_t)(32 * h), p);
+          // 2^8 in the type's bits; a NaN counts as more
+          constexpr uint32_t kMost = kBf16 ? 0x4380u : 0x5c00u;
+          const bool over = (top & 0xffffu) > kMost || (top >> 16) > kMost;
+          if (renew || !__any_sync(0xffffffffu, over)) break;
+          renew = true;
         }
+        tmem_st32(ts, reinterpret_cast<uint32_t(&)[32]>(p[0]));
+        tmem_st32(ts + 32u, reinterpret_cast<uint32_t(&)[32]>(p[32]));
         l += (l0 + l1) + (l2 + l3);
         tmem_wait_st();
         tc_fence_before();
@@ -492,21 +550,36 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         tc_fence_after();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const bool none = lim < 0;  // O holds the products of zero weights: nothing to divide
+        // through shared memory, so that a store instruction writes whole 128-byte runs
+        // (stored row by row a lane, the epilogue took 5500 cycles of an item)
+        const uint32_t out = base + SM::OUT + (uint32_t)warp * 4096u;
+        const int r_here = tl.rows - 32 * (warp & 3);
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
-          tmem_wait_ld32(o);
-          if (keeps) {
+        for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
+          for (int q = 0; q < 2; ++q) {
+            float o[32];
+            tmem_ld32_nowait(to + (uint32_t)(64 * h + 32 * q), o);
+            tmem_wait_ld32(o);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
               uint32_t w[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y)
-                w[y] = none ? 0u : Act<ACT>::pack2(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * q + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                w[y] = none ? 0u : Act<ACT>::pack2(o[8 * x + 2 * y] * inv, o[8 * x + 2 * y + 1] * inv);
+              sts_u128(out + (uint32_t)(lane * 128 + (((4 * q + x) ^ (lane & 7)) << 4)), make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
+          __syncwarp();
+          ACT* to_row = static_cast<ACT*>(a.out) + (size_t)(tl.q0 + 32 * (warp & 3)) * a.out_stride + (size_t)tl.head * D +
+                        64 * h + 8 * (lane & 7);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int r = 4 * x + (lane >> 3);
+            const uint4 w = lds_u128(out + (uint32_t)(r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+            if (r < r_here) *reinterpret_cast<uint4*>(to_row + (size_t)r * a.out_stride) = w;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       } else if (keeps) {
