@@ -22,8 +22,12 @@
 //    passes through shared memory;
 //  * warps 0-3 and 4-7 hold one query row a thread (no shuffles) and run the
 //    softmax of tile 0 and 1 in turn with the other tile's products;
-//  * one warp loads (TMA, ring of 128-key tiles of K and V), two warps issue the
-//    products, one per tile: S(j + 1) follows P V(j) in the same issue order, so
+//  * one warp loads (TMA, ring of 128-key tiles of K and V), one warp issues the
+//    products, P V(j) and S(j + 1) of one tile together, then of the other: the
+//    tiles then take turns on the tensor cores and in the softmax.  (With a warp
+//    per tile their products interleaved, both tiles ran the softmax at the same
+//    time and waited for the tensor cores at the same time: 349 us against
+//    PLACEHOLDER for the packed batch.)  S(j + 1) follows P V(j) in issue order, so
 //    its completion also tells the softmax that O is at rest.
 // With an even number of query heads per key head the two tiles are the same
 // queries of two heads (equal work, K and V read once for both), else two
@@ -46,8 +50,8 @@
 namespace ds {
 
 constexpr int kPrLoadWarp = 8;   // after the softmax warps: 0-3 of tile 0, 4-7 of tile 1
-constexpr int kPrMmaWarp = 9;    // and 10
-constexpr int kPrThreads = 11 * 32;
+constexpr int kPrMmaWarp = 9;
+constexpr int kPrThreads = 10 * 32;
 constexpr int kPrRows = 128;     // queries per tile, keys per block
 
 // One entry of the work list: a tile (or two neighbouring ones) of a sequence.
@@ -235,12 +239,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   auto s_full = [&](int t) { return bars + 8u * (2 * NST + 4 + t); };
   auto p_full = [&](int t) { return bars + 8u * (2 * NST + 6 + t); };
   auto o_full = [&](int t) { return bars + 8u * (2 * NST + 8 + t); };
-  auto done = [&](int t) { return bars + 8u * (2 * NST + 10 + t); };
+  const uint32_t done = bars + 8u * (2 * NST + 10);
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(full(i), 1);
-      mbar_init(empty(i), 2);
+      mbar_init(empty(i), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
@@ -248,8 +252,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t), 4);
       mbar_init(o_full(t), 1);
-      mbar_init(done(t), 1);
     }
+    mbar_init(done, 1);
     mbar_init_fence();
   }
   if (warp == kPrMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -352,16 +356,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint32_t p = i < st ? ph : ph ^ 1;  // parity of the stage's last use
       mbar_wait(full(i), p, a.status);
     }
-  } else if (warp == kPrMmaWarp || warp == kPrMmaWarp + 1) {
+  } else if (warp == kPrMmaWarp) {
     // ------------------------------------------------------------ products
-    const int t = warp - kPrMmaWarp;
     const uint32_t lead = elect_one();
     const uint32_t idesc_s = umma_idesc(kBf16, kPrRows), idesc_o = umma_idesc(kBf16, D) | (1u << 16);
     const uint32_t tm = (uint32_t)uni((int)tmem);
-    const uint32_t ts = tm + (uint32_t)(t * kPrRows), to = tm + (uint32_t)(2 * kPrRows + t * kPrRows);
-    const uint64_t dq = umma_desc_sw128(base + SM::Q + t * TILE);
     int st = 0;
-    uint32_t ph = 0, qph = 0, pph = 0;
+    uint32_t ph = 0, qph = 0, pph[2] = {0, 0};
     auto next_stage = [&]() {
       if (++st == NST) {
         st = 0;
@@ -375,63 +376,72 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const long long i = prompt_item(k, n_items);
       if (i < 0) break;
       const PromptItem it = items[i / hp];
-      const Tile tl = tile_of(it, (int)(i % hp), t), tr = tile_of(it, (int)(i % hp), 1 - t);
-      const int n = uni(tl.n), nkv = max(n, uni(tr.n));
+      const int n[2] = {uni(tile_of(it, (int)(i % hp), 0).n), uni(tile_of(it, (int)(i % hp), 1).n)};
+      const int nkv = max(n[0], n[1]);
       const int lk = uni(it.lk);
       if (nkv == 0) continue;
-      wait(q_full(t), qph);
+      auto product_s = [&](int t, int j, int stage) {  // S = Q K_j^T
+        const uint64_t dq = umma_desc_sw128(base + SM::Q + t * TILE), dk = umma_desc_sw128(base + SM::RING + stage * TILE);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = (uint64_t)(((kk >> 2) * (kPrRows * 128) + (kk & 3) * 32) >> 4);
+          lead_umma(lead, tm + (uint32_t)(t * kPrRows), dq + step, dk + step, idesc_s, kk > 0);
+        }
+        lead_commit(lead, s_full(t));
+        if (j == n[t] - 1) lead_commit(lead, q_empty(t));
+      };
+      // the first S of both tiles
+      int sk = st;
+      wait(full(st), ph);  // K_0
+      next_stage();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        wait(q_full(t), qph);
+        if (dead) continue;
+        tc_fence_after();
+        if (n[t] > 0) product_s(t, 0, sk);
+        else if (lead) mbar_arrive(q_empty(t));
+      }
       qph ^= 1;
-      auto product_s = [&](int j) {  // S = Q K_j^T from the ring's stage; releases it
-        wait(full(st), ph);
-        if (!dead) {
-          tc_fence_after();
-          const uint64_t dk = umma_desc_sw128(base + SM::RING + st * TILE);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t step = (uint64_t)(((kk >> 2) * (kPrRows * 128) + (kk & 3) * 32) >> 4);
-            lead_umma(lead, ts, dq + step, dk + step, idesc_s, kk > 0);
-          }
-          lead_commit(lead, s_full(t));
-          lead_commit(lead, empty(st));
-          if (j == n - 1) lead_commit(lead, q_empty(t));
-        }
-        next_stage();
-      };
-      auto pass = [&]() {  // a stage that only the other tile uses
-        wait(full(st), ph);
-        if (lead && !dead) mbar_arrive(empty(st));
-        next_stage();
-      };
-      if (n == 0 && lead && !dead) mbar_arrive(q_empty(t));
-      if (n > 0) product_s(0);
-      else pass();
+      if (!dead) lead_commit(lead, empty(sk));
       for (int j = 0; j < nkv; ++j) {
-        if (j >= n) {
-          pass();  // V_j
-          if (j + 1 < nkv) pass();
-          continue;
-        }
+        const int sv = st;
         wait(full(st), ph);  // V_j
-        wait(p_full(t), pph);
-        pph ^= 1;
-        if (!dead) {
-          tc_fence_after();
-          if (lk - j * kPrRows < kPrRows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          const uint64_t dv = umma_desc_mn_sw128(base + SM::RING + st * TILE, kPrRows * 128);
-#pragma unroll
-          for (int kk = 0; kk < kPrRows / 16; ++kk)
-            lead_umma_tmem_a(lead, to, ts + (uint32_t)(kk * 8), dv + (uint64_t)((kk * 2048) >> 4), idesc_o,
-                             (j > 0 || kk > 0));
-          if (j == n - 1) lead_commit(lead, o_full(t));
-          lead_commit(lead, empty(st));
-        }
         next_stage();
-        if (j + 1 < n) product_s(j + 1);
-        else if (j + 1 < nkv) pass();
+        const bool more = j + 1 < nkv;
+        sk = st;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= n[t]) continue;
+          wait(p_full(t), pph[t]);
+          pph[t] ^= 1;
+          if (!dead) {
+            tc_fence_after();
+            if (lk - j * kPrRows < kPrRows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            const uint64_t dv = umma_desc_mn_sw128(base + SM::RING + sv * TILE, kPrRows * 128);
+#pragma unroll
+            for (int kk = 0; kk < kPrRows / 16; ++kk)
+              lead_umma_tmem_a(lead, tm + (uint32_t)(2 * kPrRows + t * kPrRows), tm + (uint32_t)(t * kPrRows + kk * 8),
+                               dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (j > 0 || kk > 0));
+            if (j == n[t] - 1) lead_commit(lead, o_full(t));
+            if (t == 1 || j >= n[1]) lead_commit(lead, empty(sv));
+          }
+          if (j + 1 < n[t]) {
+            wait(full(sk), ph);  // K_{j+1}
+            if (!dead) {
+              tc_fence_after();
+              product_s(t, j + 1, sk);
+            }
+          }
+        }
+        if (more) {
+          if (!dead) lead_commit(lead, empty(sk));
+          next_stage();
+        }
       }
     }
-    lead_commit(lead, done(t));
-    mbar_wait(done(t), 0, a.status);
+    lead_commit(lead, done);
+    mbar_wait(done, 0, a.status);
   } else {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;
