@@ -296,6 +296,8 @@ ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void*
   DS_TRY(check_batch(q_tokens, batch, cu_q, cu_k));
   if (k_tokens < 0 || k_tokens > (1 << 24)) return fail(DS_ERR_INVALID_ARG, "k_tokens must be in 0 .. 2^24");
   if (!std::isfinite(scale) || scale <= 0.f) return fail(DS_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (((long long)q_tokens / 128 + batch + 2) * heads >= (1LL << 31) - 65536)
+    return fail(DS_ERR_UNSUPPORTED, "too many (tile, head) pairs in one call");
   DS_TRY(check_ws(workspace, ws_bytes, prompt_attention_ws_bytes(heads, batch, q_tokens)));
   if (q_tokens == 0) return DS_OK;
   DS_TRY(check_packed(q, q_stride, heads, head_dim));

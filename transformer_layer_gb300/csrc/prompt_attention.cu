@@ -130,9 +130,14 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* v) {
 }
 // (the loaded registers are tied to the wait, so that no use of them moves before it)
 __device__ __forceinline__ void tmem_wait_ld32(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]),
+                 "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                 "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ float pr_ex2(float x) {
@@ -140,24 +145,45 @@ __device__ __forceinline__ float pr_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
 }
-// (x0, x1) * c + d and (a0, a1) + (b0, b1), two lanes of one instruction
-__device__ __forceinline__ void fma2(float& x0, float& x1, float c, float d) {
-  asm("{\n .reg .b64 x, c, d;\n mov.b64 x, {%0, %1};\n mov.b64 c, {%2, %2};\n mov.b64 d, {%3, %3};\n"
-      " fma.rn.f32x2 x, x, c, d;\n mov.b64 {%0, %1}, x;\n}\n"
-      : "+f"(x0), "+f"(x1)
-      : "f"(c), "f"(d));
+// Two fp32 lanes of one instruction; constants come as pairs built once.
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
 }
-__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
-      " mov.b64 {%0, %1}, a;\n}\n"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
+// 2^(x c + d) of two values, as a pair (kept a pair: as two floats, the compiler
+// moved every weight once more to add it up).
+__device__ __forceinline__ uint64_t ex2_pair(float x0, float x1, uint64_t c, uint64_t d) {
+  uint64_t r;
+  asm("{\n .reg .b64 x;\n .reg .f32 a, b;\n mov.b64 x, {%1, %2};\n fma.rn.f32x2 x, x, %3, %4;\n mov.b64 {a, b}, x;\n"
+      " ex2.approx.ftz.f32 a, a;\n ex2.approx.ftz.f32 b, b;\n mov.b64 %0, {a, b};\n}\n"
+      : "=l"(r)
+      : "f"(x0), "f"(x1), "l"(c), "l"(d));
+  return r;
 }
-__device__ __forceinline__ void mul2(float& a0, float& a1, float b) {
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mul.rn.f32x2 a, a, b;\n"
-      " mov.b64 {%0, %1}, a;\n}\n"
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum_pair(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+template <typename ACT>
+__device__ __forceinline__ uint32_t round_pair(uint64_t a) {
+  uint32_t r;
+  if constexpr (std::is_same<ACT, __half>::value)
+    asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n cvt.rn.f16x2.f32 %0, b, a;\n}\n" : "=r"(r) : "l"(a));
+  else
+    asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n cvt.rn.bf16x2.f32 %0, b, a;\n}\n" : "=r"(r) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ void mul2(float& a0, float& a1, uint64_t b) {
+  asm("{\n .reg .b64 a;\n mov.b64 a, {%0, %1};\n mul.rn.f32x2 a, a, %2;\n mov.b64 {%0, %1}, a;\n}\n"
       : "+f"(a0), "+f"(a1)
-      : "f"(b));
+      : "l"(b));
 }
 
 // Lane 0's value, known to the compiler as the same for the whole warp: loops and
@@ -213,9 +239,9 @@ struct PromptSmem {
 
 // A CTA's k-th item of n: rounds of `grid` items taken in alternating direction,
 // so that the longer items of one round meet the shorter ones of the next.
-__device__ __forceinline__ long long prompt_item(int k, long long n) {
+__device__ __forceinline__ int prompt_item(int k, int n) {
   const int g = gridDim.x, c = blockIdx.x;
-  const long long i = (long long)k * g + ((k & 1) ? g - 1 - c : c);
+  const int i = k * g + ((k & 1) ? g - 1 - c : c);  // (the launch keeps n + 2 g below 2^31)
   return i < n ? i : -1;
 }
 
@@ -266,9 +292,30 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
   const int group = a.heads / a.kv_heads;
   const int hp = pair_heads ? a.heads / 2 : a.heads;  // items per list entry
-  const long long n_items = (long long)uni(list->count) * hp;
+  const int n_items = uni(list->count) * hp;
   bool dead = false;  // a wait of this warp gave up: nothing more is waited for or issued
 
+  // The k-th item of this CTA, one ahead: its entry is loaded while the previous one runs.
+  struct Next {
+    PromptItem it;
+    int head;  // head, or pair of heads; -1: no item
+  };
+  auto fetch = [&](int k) {
+    Next x;
+    const int i = prompt_item(k, n_items);
+    x.head = -1;
+    if (i >= 0) {
+      const int e = i / hp;
+      x.head = i - e * hp;
+      const int4 u = *reinterpret_cast<const int4*>(items + e);
+      x.it.q0 = u.x;
+      x.it.rows = u.y;
+      x.it.k0 = u.z;
+      x.it.lk = u.w;
+      x.it.lim = items[e].lim;
+    }
+    return x;
+  };
   // What an item means for tile t.
   struct Tile {
     int q0, rows, head, lim, n;
@@ -297,11 +344,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     };
     int used = 0;
-    for (int k = 0;; ++k) {
-      const long long i = prompt_item(k, n_items);
-      if (i < 0) break;
-      const PromptItem it = items[i / hp];
-      const Tile t0 = tile_of(it, (int)(i % hp), 0), t1 = tile_of(it, (int)(i % hp), 1);
+    Next next = fetch(0);
+    for (int k = 1; next.head >= 0; ++k) {
+      const PromptItem it = next.it;
+      const Tile t0 = tile_of(it, next.head, 0), t1 = tile_of(it, next.head, 1);
+      next = fetch(k);
       const int n = max(t0.n, t1.n);
       const int kvh = t0.head / group;
       for (int j = 0; j < n; ++j) {
@@ -372,11 +419,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar, parity, a.status));
     };
-    for (int k = 0;; ++k) {
-      const long long i = prompt_item(k, n_items);
-      if (i < 0) break;
-      const PromptItem it = items[i / hp];
-      const int n[2] = {uni(tile_of(it, (int)(i % hp), 0).n), uni(tile_of(it, (int)(i % hp), 1).n)};
+    Next next = fetch(0);
+    for (int k = 1; uni(next.head) >= 0; ++k) {
+      const PromptItem it = next.it;
+      const int n[2] = {uni(tile_of(it, next.head, 0).n), uni(tile_of(it, next.head, 1).n)};
+      next = fetch(k);
       const int nkv = max(n[0], n[1]);
       const int lk = uni(it.lk);
       if (nkv == 0) continue;
@@ -451,11 +498,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int row = 32 * (warp & 3) + lane;
     const float c = a.scale_log2;
     uint32_t sph = 0, oph = 0;
-    for (int k = 0;; ++k) {
-      const long long i = prompt_item(k, n_items);
-      if (i < 0) break;
-      const PromptItem it = items[i / hp];
-      const Tile tl = tile_of(it, (int)(i % hp), t);
+    Next next = fetch(0);
+    for (int k = 1; next.head >= 0; ++k) {
+      const PromptItem it = next.it;
+      const Tile tl = tile_of(it, next.head, t);
+      next = fetch(k);
       float m = -INFINITY, l = 0.f;
       const int lim = min(it.lk - 1, tl.lim + row);  // last key this row sees
       for (int j = 0; j < tl.n; ++j) {
@@ -464,18 +511,24 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         sph ^= 1;
         if (dead) continue;
         tc_fence_after();
-        // some row of the tile sees less than the whole block
-        const bool masked = min(it.lk - 1, tl.lim) < (j + 1) * kPrRows - 1;
-        const int last = lim - j * kPrRows;
-        auto mask = [&](float* v, int q) {
-          if (masked) {
+        // Where some row of the tile sees less than the whole block, S is masked in place
+        // first (selected in the pass below, it cost a copy of every score in every block).
+        if (min(it.lk - 1, tl.lim) < (j + 1) * kPrRows - 1) {
+          const int last = lim - j * kPrRows;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float v[32];
+            tmem_ld32_nowait(ts + (uint32_t)(32 * q), v);
+            tmem_wait_ld32(v);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (32 * q + x > last) v[x] = -INFINITY;
+            tmem_st32(ts + (uint32_t)(32 * q), reinterpret_cast<uint32_t(&)[32]>(v));
           }
-        };
+          tmem_wait_st();
+        }
         uint32_t p[kPrRows / 2];
-        float l0, l1, l2, l3;
+        uint64_t l0, l1;
         // The weights are computed relative to the reference as it is; only where one
         // comes out above 2^8 (or there is no reference yet) does the true maximum
         // of the rows matter: it is taken, l and O are rescaled, and the weights are
@@ -488,7 +541,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               float v[32];
               tmem_ld32_nowait(ts + (uint32_t)(32 * q), v);
               tmem_wait_ld32(v);
-              mask(v, q);
 #pragma unroll
               for (int x = 0; x < 32; x += 8)
 #pragma unroll
@@ -505,13 +557,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
                 tmem_wait_ld32(o);
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) mul2(o[x], o[x + 1], al);
+                for (int x = 0; x < 32; x += 2) mul2(o[x], o[x + 1], twice(al));
                 tmem_st32(to + (uint32_t)(32 * q), reinterpret_cast<uint32_t(&)[32]>(o));
               }
             }
           }
-          const float mc = m == -INFINITY ? 0.f : -m * c;
-          l0 = l1 = l2 = l3 = 0.f;
+          const uint64_t mc = twice(m == -INFINITY ? 0.f : -m * c), cc = twice(c);
+          l0 = l1 = 0ull;  // (two zeros)
           uint32_t top = 0;  // largest weight of each half, as 16-bit patterns (weights are positive)
           float v[2][32];
           tmem_ld32_nowait(ts, v[0]);
@@ -520,18 +572,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             float* w = v[q & 1];
             tmem_wait_ld32(w);
             if (q < 3) tmem_ld32_nowait(ts + (uint32_t)(32 * (q + 1)), v[(q + 1) & 1]);
-            mask(w, q);
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
-              fma2(w[x], w[x + 1], c, mc);
-              fma2(w[x + 2], w[x + 3], c, mc);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) w[x + y] = pr_ex2(w[x + y]);
-              add2(l0, l1, w[x], w[x + 1]);
-              add2(l2, l3, w[x + 2], w[x + 3]);
+              const uint64_t e0 = ex2_pair(w[x], w[x + 1], cc, mc), e1 = ex2_pair(w[x + 2], w[x + 3], cc, mc);
+              l0 = add_pair(l0, e0);
+              l1 = add_pair(l1, e1);
               const int at = 16 * q + x / 2;
-              p[at] = Act<ACT>::pack2(w[x], w[x + 1]);
-              p[at + 1] = Act<ACT>::pack2(w[x + 2], w[x + 3]);
+              p[at] = round_pair<ACT>(e0);
+              p[at + 1] = round_pair<ACT>(e1);
               top = __vimax3_s16x2(top, p[at], p[at + 1]);
             }
           }
@@ -543,7 +591,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         tmem_st32(ts, reinterpret_cast<uint32_t(&)[32]>(p[0]));
         tmem_st32(ts + 32u, reinterpret_cast<uint32_t(&)[32]>(p[32]));
-        l += (l0 + l1) + (l2 + l3);
+        l += sum_pair(add_pair(l0, l1));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -566,10 +614,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int r_here = tl.rows - 32 * (warp & 3);
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h) {
+          float both[2][32];
+          tmem_ld32_nowait(to + (uint32_t)(64 * h), both[0]);
+          tmem_ld32_nowait(to + (uint32_t)(64 * h + 32), both[1]);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            float o[32];
-            tmem_ld32_nowait(to + (uint32_t)(64 * h + 32 * q), o);
+            float* o = both[q];
             tmem_wait_ld32(o);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -648,6 +698,7 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
   e = cudaLaunchKernelEx(&cfg, prompt_list_kernel, a, pair ? kPrRows : 2 * kPrRows, list, items, most);
   if (e != cudaSuccess) return e;
   const long long ctas = (long long)most * (pair ? a.heads / 2 : a.heads);
+  if (ctas + 2LL * num_sms >= 2147483647LL) return cudaErrorInvalidValue;  // (refused by the entry point)
   cfg.gridDim = dim3((unsigned)(ctas < num_sms ? ctas : num_sms));
   cfg.blockDim = dim3(kPrThreads);
   cfg.dynamicSmemBytes = PromptSmem<D>::TOTAL;
