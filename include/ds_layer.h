@@ -505,7 +505,9 @@ DS_API ds_status ds_paged_attention(const ds_paged_cache* cache, const void* q, 
                                     int64_t q_stride, int64_t out_stride, const int32_t* past_len, int batch,
                                     int new_tokens, float scale, void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace of ds_prompt_attention for packed q of `tokens` rows. */
+/* Bytes of workspace of ds_prompt_attention on the current device for packed q
+ * of `tokens` rows; 0 for invalid arguments.  Zero-filled once
+ * (ds_workspace_init). */
 DS_API size_t ds_prompt_attention_workspace_bytes(int heads, int batch, int tokens);
 
 /* Causal attention over packed prompts: sequence b has Lq = cu_q[b+1] -

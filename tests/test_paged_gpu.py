@@ -401,6 +401,9 @@ PROMPTS = [
     (BF16, 5, 5, 128, [17, 300], [18, 299]),          # the second: more queries than keys
     (BF16, 8, 1, 64, [40, 7, 140], [0, 2, 513]),      # no keys at all
     (F16, 16, 4, 128, [384], [2000]),
+    (BF16, 2, 1, 64, [3, 300], [20000, 9000]),        # few rows, long keys: items shared by many CTAs
+    (F16, 3, 3, 128, [1], [30001]),
+    (BF16, 1, 1, 128, [250, 1, 700], [5000, 4000, 700]),
 ]
 
 

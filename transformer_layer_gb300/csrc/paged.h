@@ -70,7 +70,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, int num_sms, cudaStrea
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, int num_sms, cudaStream_t st);
 size_t paged_attention_ws_bytes(const PagedView& c, int heads, int batch, int T, int num_sms);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, int num_sms, cudaStream_t st);
-size_t prompt_attention_ws_bytes(int heads, int batch, int tokens);
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st);
+size_t prompt_attention_ws_bytes(int batch, int tokens, int num_sms);
+// *kernels: how many were launched.
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st, int* kernels);
 
 }  // namespace ds

@@ -255,15 +255,16 @@ ds_status ds_paged_attention(const ds_paged_cache* cache, const void* q, void* o
   DS_TRY(check_packed(out, out_stride, heads, cache->head_dim));
   if (q == out) return fail(DS_ERR_INVALID_ARG, "out must not alias q");
   if (!multiple_of(past_len, 4)) return fail(DS_ERR_INVALID_ARG, "past_len must be a non-null int32 device array");
+  DS_TRY(check_ws(workspace, ws_bytes, 0));
   int dev = -1;
   const int sms = device_sms(&dev);
   if (sms == 0) return fail(DS_ERR_CUDA, "no CUDA device");
   PagedAttnArgs a;
   a.c = view(cache);
-  DS_TRY(check_ws(workspace, ws_bytes, paged_attention_ws_bytes(a.c, heads, batch, new_tokens, sms)));
   DS_TRY(check_cache_device(cache, dev));
   if (!on_device(q, dev) || !on_device(out, dev) || !on_device(past_len, dev) || !on_device(workspace, dev))
     return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  DS_TRY(check_ws(workspace, ws_bytes, paged_attention_ws_bytes(a.c, heads, batch, new_tokens, sms)));
   a.q = q;
   a.out = out;
   a.q_stride = q_stride;
@@ -280,7 +281,9 @@ ds_status ds_paged_attention(const ds_paged_cache* cache, const void* q, void* o
 
 size_t ds_prompt_attention_workspace_bytes(int heads, int batch, int tokens) {
   if (heads < 1 || heads > 65535 || batch < 1 || batch > 65535 || tokens < 0 || tokens > (1 << 24)) return 0;
-  return prompt_attention_ws_bytes(heads, batch, tokens);
+  int dev = -1;
+  const int sms = device_sms(&dev);
+  return sms == 0 ? 0 : prompt_attention_ws_bytes(batch, tokens, sms);
 }
 
 ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void* out, int heads, int kv_heads,
@@ -298,7 +301,7 @@ ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void*
   if (!std::isfinite(scale) || scale <= 0.f) return fail(DS_ERR_INVALID_ARG, "scale must be positive and finite");
   if (((long long)q_tokens / 128 + batch + 2) * heads >= (1LL << 31) - 65536)
     return fail(DS_ERR_UNSUPPORTED, "too many (tile, head) pairs in one call");
-  DS_TRY(check_ws(workspace, ws_bytes, prompt_attention_ws_bytes(heads, batch, q_tokens)));
+  DS_TRY(check_ws(workspace, ws_bytes, 256));
   if (q_tokens == 0) return DS_OK;
   DS_TRY(check_packed(q, q_stride, heads, head_dim));
   DS_TRY(check_packed(out, out_stride, heads, head_dim));
@@ -313,6 +316,7 @@ ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void*
   if (!on_device(q, dev) || !on_device(out, dev) || !on_device(cu_q, dev) || !on_device(cu_k, dev) ||
       !on_device(workspace, dev) || (k_tokens > 0 && (!on_device(k, dev) || !on_device(v, dev))))
     return fail(DS_ERR_INVALID_ARG, kNotDevice);
+  DS_TRY(check_ws(workspace, ws_bytes, prompt_attention_ws_bytes(batch, q_tokens, sms)));
   PromptAttnArgs a;
   a.q = q;
   a.k = k;
@@ -333,8 +337,9 @@ ds_status ds_prompt_attention(const void* q, const void* k, const void* v, void*
   a.cu_k = cu_k;
   a.scale_log2 = scale_log2(scale);
   a.status = static_cast<unsigned*>(workspace);
-  return launched(launch_prompt_attention(a, workspace, sms, static_cast<cudaStream_t>(stream)),
-                  "prompt attention launch", 2);
+  int kernels = 0;
+  const cudaError_t e = launch_prompt_attention(a, workspace, sms, static_cast<cudaStream_t>(stream), &kernels);
+  return launched(e, "prompt attention launch", kernels);
 }
 
 }  // extern "C"

@@ -27,7 +27,7 @@
 //    tiles then take turns on the tensor cores and in the softmax.  (With a warp
 //    per tile their products interleaved, both tiles ran the softmax at the same
 //    time and waited for the tensor cores at the same time: 349 us against
-//    PLACEHOLDER for the packed batch.)  S(j + 1) follows P V(j) in issue order, so
+//    267 for nine prompts of 500 to 4096 tokens.)  S(j + 1) follows P V(j) in issue order, so
 //    its completion also tells the softmax that O is at rest.
 // With an even number of query heads per key head the two tiles are the same
 // queries of two heads (equal work, K and V read once for both), else two
@@ -36,8 +36,11 @@
 // by position, and V rows behind the sequence are zero-filled (that block of V
 // comes by cp.async), so that nothing of one sequence reaches another.
 //
-// Split: a first small kernel lists the query tiles, longest first; CTAs (one
-// per SM) take items of (tile, head pair) in alternating order.
+// Split: with many items (tile, head pair) a first small kernel lists the tiles,
+// longest first, and CTAs (one per SM) take whole items in alternating order.
+// With few, every CTA takes the same number of key blocks of all items laid end
+// to end (prompt_split.h); an item that crosses CTAs leaves partial O, m and l
+// in the workspace, and the last CTA to arrive joins them in order.
 #include <cuda.h>
 
 #include <atomic>
@@ -45,6 +48,7 @@
 #include <type_traits>
 
 #include "paged.cuh"
+#include "prompt_split.h"
 #include "tcgen05.cuh"
 
 namespace ds {
@@ -54,13 +58,10 @@ constexpr int kPrMmaWarp = 9;
 constexpr int kPrThreads = 10 * 32;
 constexpr int kPrRows = 128;     // queries per tile, keys per block
 
-// One entry of the work list: a tile (or two neighbouring ones) of a sequence.
-struct PromptItem {
-  int q0;     // first packed query row
-  int rows;   // queries from there on (up to 128, or 256 for two tiles)
-  int k0;     // first packed key row of the sequence
-  int lk;     // its keys
-  int lim;    // last key that the first query sees (may be negative)
+// A list entry: tile t of a sequence.
+struct PromptEntry {
+  PromptSeq s;
+  int t;
   int pad[3];
 };
 struct PromptList {
@@ -68,10 +69,20 @@ struct PromptList {
   int pad[63];
 };
 
+__device__ __forceinline__ PromptSeq prompt_seq(const PromptAttnArgs& a, int b) {
+  PromptSeq s;
+  s.q0 = max(0, a.cu_q[b]);
+  s.lq = max(0, min(a.cu_q[b + 1], a.q_tokens) - s.q0);
+  s.k0 = max(0, a.cu_k[b]);
+  s.lk = max(0, min(a.cu_k[b + 1], a.k_tokens) - s.k0);
+  return s;
+}
+
 // Lists the tiles of `unit` queries of all sequences, most key blocks first
-// (counting sort, the last bucket for 1023 blocks or more).
+// (counting sort, the first bucket for 1023 blocks or more; the order inside a
+// bucket may differ from launch to launch, the results do not).
 __global__ void __launch_bounds__(1024) prompt_list_kernel(const PromptAttnArgs a, int unit, PromptList* list,
-                                                           PromptItem* items, int most) {
+                                                           PromptEntry* entries, int most) {
   __shared__ int hist[1024], s_warp[32];
   pdl_wait();
   pdl_launch_dependents();
@@ -80,22 +91,13 @@ __global__ void __launch_bounds__(1024) prompt_list_kernel(const PromptAttnArgs 
   __syncthreads();
   auto each = [&](auto&& f) {
     for (int b = warp; b < a.batch; b += 32) {
-      const int q0 = max(0, a.cu_q[b]), q1 = min(a.cu_q[b + 1], a.q_tokens);
-      const int k0 = max(0, a.cu_k[b]), lk = max(0, min(a.cu_k[b + 1], a.k_tokens) - k0);
-      const int lq = q1 - q0;
-      for (int t = lane; t * unit < lq; t += 32) {
-        PromptItem it = {};
-        it.q0 = q0 + t * unit;
-        it.rows = min(unit, lq - t * unit);
-        it.k0 = k0;
-        it.lk = lk;
-        it.lim = lk - lq + t * unit;
-        const int seen = max(0, min(lk, it.lim + it.rows));
-        f(it, 1023 - min(1023, (seen + kPrRows - 1) / kPrRows));
-      }
+      PromptEntry e = {};
+      e.s = prompt_seq(a, b);
+      const int T = prompt_tiles(e.s, unit);
+      for (e.t = lane; e.t < T; e.t += 32) f(e, 1023 - min(1023, prompt_blocks(e.s, unit, e.t)));
     }
   };
-  each([&](const PromptItem&, int key) { atomicAdd(&hist[key], 1); });
+  each([&](const PromptEntry&, int key) { atomicAdd(&hist[key], 1); });
   __syncthreads();
   const int n = hist[tid];
   int inc = n;
@@ -111,9 +113,9 @@ __global__ void __launch_bounds__(1024) prompt_list_kernel(const PromptAttnArgs 
   hist[tid] = before + inc - n;
   if (tid == 1023) list->count = min(before + inc, most);
   __syncthreads();
-  each([&](const PromptItem& it, int key) {
+  each([&](const PromptEntry& e, int key) {
     const int at = atomicAdd(&hist[key], 1);
-    if (at < most) items[at] = it;
+    if (at < most) entries[at] = e;
   });
 }
 
@@ -237,24 +239,39 @@ struct PromptSmem {
   static constexpr int TOTAL = BARS + 256 + 1024;  // and the alignment of the base
 };
 
-// A CTA's k-th item of n: rounds of `grid` items taken in alternating direction,
-// so that the longer items of one round meet the shorter ones of the next.
-__device__ __forceinline__ int prompt_item(int k, int n) {
+// With a list, a CTA's k-th item of n: rounds of `grid` items taken in
+// alternating direction, so that the longer items of one round meet the shorter
+// ones of the next.
+__device__ __forceinline__ int prompt_listed(int k, int n) {
   const int g = gridDim.x, c = blockIdx.x;
   const int i = k * g + ((k & 1) ? g - 1 - c : c);  // (the launch keeps n + 2 g below 2^31)
   return i < n ? i : -1;
 }
 
-template <typename ACT, int D>
+// Parts of items that several CTAs share: of each CTA a part that continues an
+// item (0) and one that a later CTA continues (1), of both tiles.
+template <int D>
+struct PromptPart {
+  static constexpr size_t O = (size_t)kPrRows * D * 4;  // [D / 4][row] float4
+  static constexpr size_t BYTES = 2 * (O + kPrRows * 8);  // and [row] (m, l); two tiles
+};
+
+// LISTED: whole items from the list (counters and parts are not used), else shares.
+template <typename ACT, int D, bool LISTED>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                             const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptAttnArgs a,
-                            const PromptList* list, const PromptItem* items, int pair_heads) {
+                            int pair_heads, const PromptList* list, int* counters, unsigned char* parts) {
   using SM = PromptSmem<D>;
   constexpr int NST = SM::NST, TILE = SM::TILE;
   constexpr bool kBf16 = std::is_same<ACT, __nv_bfloat16>::value;
   extern __shared__ unsigned char raw[];
   __shared__ uint32_t s_tmem;
+  __shared__ long long s_scan[kPrThreads / 32];
+  __shared__ long long s_items[kPrThreads / 32];
+  __shared__ int s_longest[kPrThreads / 32];
+  __shared__ PromptBound s_bound[2];
+  __shared__ int s_last[2];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t bars = base + SM::BARS;
@@ -291,43 +308,134 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   pdl_launch_dependents();
 
   const int group = a.heads / a.kv_heads;
-  const int hp = pair_heads ? a.heads / 2 : a.heads;  // items per list entry
-  const int n_items = uni(list->count) * hp;
+  const int unit = pair_heads ? kPrRows : 2 * kPrRows;
+  const int hp = pair_heads ? a.heads / 2 : a.heads;  // items per tile
   bool dead = false;  // a wait of this warp gave up: nothing more is waited for or issued
 
-  // The k-th item of this CTA, one ahead: its entry is loaded while the previous one runs.
-  struct Next {
-    PromptItem it;
-    int head;  // head, or pair of heads; -1: no item
-  };
-  auto fetch = [&](int k) {
-    Next x;
-    const int i = prompt_item(k, n_items);
-    x.head = -1;
+  // ---- this CTA's share of the items (prompt_split.h), unless they are listed
+  auto seq_of = [&](int b) { return prompt_seq(a, b); };
+  PromptPlan plan;
+  if constexpr (!LISTED) {
+    const int per = (a.batch + kPrThreads - 1) / kPrThreads, b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+    auto units_of = [&](const PromptSeq& s) { return hp * prompt_units(s, unit, prompt_tiles(s, unit)); };
+    auto items_of = [&](const PromptSeq& s) { return (long long)hp * prompt_tiles(s, unit); };
+    long long sum = 0, sum_items = 0;
+    int longest = 0;
+    for (int b = b0; b < b1; ++b) {
+      const PromptSeq s = seq_of(b);
+      sum += units_of(s);
+      sum_items += items_of(s);
+      if (s.lq > 0) longest = max(longest, (s.lk + kPrRows - 1) / kPrRows);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    long long inc = sum, inc_items = sum_items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      const long long vi = __shfl_up_sync(0xffffffffu, inc_items, o);
+      if (lane >= o) {
+        inc += v;
+        inc_items += vi;
+      }
+    }
+    if (lane == 31) {
+      s_scan[warp] = inc;
+      s_items[warp] = inc_items;
+      s_longest[warp] = longest;
+    }
+    if (tid < 2) s_bound[tid].b = a.batch;  // behind the last item
+    __syncthreads();
+    long long before = inc - sum, total = 0, before_items = inc_items - sum_items, items = 0;
+#pragma unroll
+    for (int w = 0; w < kPrThreads / 32; ++w) {
+      if (w < warp) {
+        before += s_scan[w];
+        before_items += s_items[w];
+      }
+      total += s_scan[w];
+      items += s_items[w];
+      longest = max(longest, s_longest[w]);
+    }
+    plan = prompt_plan(total, items, gridDim.x, longest);
+    if (plan.flat) {
+      before = before_items;
+      sum = sum_items;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const long long u = ((long long)blockIdx.x + i) * plan.chunk;
+      if (u < before || u >= before + sum) continue;
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const PromptSeq s = seq_of(b);
+        const long long n = plan.flat ? items_of(s) : units_of(s);
+        if (u < at + n) {
+          s_bound[i] = prompt_locate(s, unit, plan, b, at, u - at);
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+  }
+  // f(item, first block, end block, ahead) for each item of the share; f calls
+  // ahead() once, which looks the next one up (early, to hide the look-up; the
+  // softmax late, when it has registers for it).
+  using Item = PromptItem;
+  PromptBound till;
+  if constexpr (!LISTED) till = s_bound[1];
+  const int n_listed = LISTED ? uni(list->count) * hp : 0;
+  auto listed = [&](int k) {
+    Item x;
+    const int i = prompt_listed(k, n_listed);
+    x.b = i < 0 ? a.batch : 0;
     if (i >= 0) {
-      const int e = i / hp;
-      x.head = i - e * hp;
-      const int4 u = *reinterpret_cast<const int4*>(items + e);
-      x.it.q0 = u.x;
-      x.it.rows = u.y;
-      x.it.k0 = u.z;
-      x.it.lk = u.w;
-      x.it.lim = items[e].lim;
+      const PromptEntry* e = reinterpret_cast<const PromptEntry*>(list + 1) + i / hp;
+      x.h = i % hp;
+      const int4 v = *reinterpret_cast<const int4*>(&e->s);
+      x.s.q0 = v.x;
+      x.s.lq = v.y;
+      x.s.k0 = v.z;
+      x.s.lk = v.w;
+      x.t = e->t;
+      x.n = prompt_blocks(x.s, unit, x.t);
     }
     return x;
+  };
+  auto for_items = [&](auto&& f) {
+    if constexpr (LISTED) {
+      Item x = listed(0);
+      for (int k = 1; uni(x.b) < a.batch; ++k) {
+        Item next;
+        f(x, 0, x.n, [&]() { next = listed(k); });
+        x = next;
+      }
+    } else {
+      int j0;
+      Item x = prompt_first(s_bound[0], till, plan, a.batch, unit, hp, seq_of, &j0);
+      while (uni(x.b) < a.batch) {
+        const bool last = uni(prompt_last(x, till)) != 0;
+        if (last && till.j <= j0) break;
+        Item next;
+        f(x, j0, last ? till.j : x.n, [&]() { next = prompt_after(x, plan, a.batch, unit, hp, seq_of); });
+        if (last) break;
+        x = next;
+        j0 = 0;
+      }
+    }
   };
   // What an item means for tile t.
   struct Tile {
     int q0, rows, head, lim, n;
   };
-  auto tile_of = [&](const PromptItem& it, int h, int t) {
+  auto tile_of = [&](const Item& it, int t) {
     Tile r;
-    const int skip = pair_heads ? 0 : t * kPrRows;
-    r.q0 = it.q0 + skip;
-    r.rows = max(0, min(kPrRows, it.rows - skip));
-    r.head = pair_heads ? 2 * h + t : h;
-    r.lim = it.lim + skip;
-    const int seen = r.rows > 0 ? max(0, min(it.lk, r.lim + r.rows)) : 0;
+    const int skip = it.t * unit + (pair_heads ? 0 : t * kPrRows);
+    r.q0 = it.s.q0 + skip;
+    r.rows = max(0, min(kPrRows, it.s.lq - skip));
+    r.head = pair_heads ? 2 * it.h + t : it.h;
+    r.lim = it.s.lk - it.s.lq + skip;  // last key that the first query sees (may be negative)
+    const int seen = r.rows > 0 ? max(0, min(it.s.lk, r.lim + r.rows)) : 0;
     r.n = (seen + kPrRows - 1) / kPrRows;
     return r;
   };
@@ -344,15 +452,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     };
     int used = 0;
-    Next next = fetch(0);
-    for (int k = 1; next.head >= 0; ++k) {
-      const PromptItem it = next.it;
-      const Tile t0 = tile_of(it, next.head, 0), t1 = tile_of(it, next.head, 1);
-      next = fetch(k);
-      const int n = max(t0.n, t1.n);
+    for_items([&](const Item& it, int j0, int j1, auto&& ahead) {
+      ahead();
+      const Tile t0 = tile_of(it, 0), t1 = tile_of(it, 1);
+      const int n = min(j1, max(t0.n, t1.n));
       const int kvh = t0.head / group;
-      for (int j = 0; j < n; ++j) {
-        if (j == 0) {
+      for (int j = j0; j < n; ++j) {
+        if (j == j0) {
           for (int t = 0; t < 2; ++t) {
             const Tile& tt = t ? t1 : t0;
             if (!dead) dead = !mbar_wait(q_empty(t), qph ^ 1, a.status);
@@ -371,7 +477,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           dead = __any_sync(0xffffffffu, dead);
           if (!dead) {
             const uint32_t dst = base + SM::RING + st * TILE;
-            const int row0 = it.k0 + j * kPrRows, valid = it.lk - j * kPrRows;
+            const int row0 = it.s.k0 + j * kPrRows, valid = it.s.lk - j * kPrRows;
             if (kv == 0 || valid >= kPrRows) {
               if (lane == 0) {
                 mbar_arrive_expect_tx(full(st), TILE);
@@ -397,7 +503,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
       }
-    }
+    });
     // every copy has landed before the CTA may end (a reader that gave up did not wait)
     for (int i = 0; i < used; ++i) {
       const uint32_t p = i < st ? ph : ph ^ 1;  // parity of the stage's last use
@@ -419,14 +525,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar, parity, a.status));
     };
-    Next next = fetch(0);
-    for (int k = 1; uni(next.head) >= 0; ++k) {
-      const PromptItem it = next.it;
-      const int n[2] = {uni(tile_of(it, next.head, 0).n), uni(tile_of(it, next.head, 1).n)};
-      next = fetch(k);
+    for_items([&](const Item& it, int first, int j1, auto&& ahead) {
+      ahead();
+      const int j0 = uni(first);
+      const int n[2] = {uni(min(j1, tile_of(it, 0).n)), uni(min(j1, tile_of(it, 1).n))};
       const int nkv = max(n[0], n[1]);
-      const int lk = uni(it.lk);
-      if (nkv == 0) continue;
+      const int lk = uni(it.s.lk);
+      if (nkv <= j0) return;
       auto product_s = [&](int t, int j, int stage) {  // S = Q K_j^T
         const uint64_t dq = umma_desc_sw128(base + SM::Q + t * TILE), dk = umma_desc_sw128(base + SM::RING + stage * TILE);
 #pragma unroll
@@ -439,19 +544,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       };
       // the first S of both tiles
       int sk = st;
-      wait(full(st), ph);  // K_0
+      wait(full(st), ph);  // the first K
       next_stage();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         wait(q_full(t), qph);
         if (dead) continue;
         tc_fence_after();
-        if (n[t] > 0) product_s(t, 0, sk);
+        if (n[t] > j0) product_s(t, j0, sk);
         else if (lead) mbar_arrive(q_empty(t));
       }
       qph ^= 1;
       if (!dead) lead_commit(lead, empty(sk));
-      for (int j = 0; j < nkv; ++j) {
+      for (int j = j0; j < nkv; ++j) {
         const int sv = st;
         wait(full(st), ph);  // V_j
         next_stage();
@@ -469,7 +574,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kPrRows / 16; ++kk)
               lead_umma_tmem_a(lead, tm + (uint32_t)(2 * kPrRows + t * kPrRows), tm + (uint32_t)(t * kPrRows + kk * 8),
-                               dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (j > 0 || kk > 0));
+                               dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (j > j0 || kk > 0));
             if (j == n[t] - 1) lead_commit(lead, o_full(t));
             if (t == 1 || j >= n[1]) lead_commit(lead, empty(sv));
           }
@@ -486,7 +591,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           next_stage();
         }
       }
-    }
+    });
     lead_commit(lead, done);
     mbar_wait(done, 0, a.status);
   } else {
@@ -498,14 +603,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int row = 32 * (warp & 3) + lane;
     const float c = a.scale_log2;
     uint32_t sph = 0, oph = 0;
-    Next next = fetch(0);
-    for (int k = 1; next.head >= 0; ++k) {
-      const PromptItem it = next.it;
-      const Tile tl = tile_of(it, next.head, t);
-      next = fetch(k);
+    for_items([&](const Item& it, int j0, int j1, auto&& ahead) {
+      const Tile tl = tile_of(it, t);
+      const int n = min(j1, tl.n);
       float m = -INFINITY, l = 0.f;
-      const int lim = min(it.lk - 1, tl.lim + row);  // last key this row sees
-      for (int j = 0; j < tl.n; ++j) {
+      const int lim = min(it.s.lk - 1, tl.lim + row);  // last key this row sees
+      for (int j = j0; j < n; ++j) {
         if (!dead) dead = !mbar_wait(s_full(t), sph, a.status);
         dead = __any_sync(0xffffffffu, dead);
         sph ^= 1;
@@ -513,7 +616,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         tc_fence_after();
         // Where some row of the tile sees less than the whole block, S is masked in place
         // first (selected in the pass below, it cost a copy of every score in every block).
-        if (min(it.lk - 1, tl.lim) < (j + 1) * kPrRows - 1) {
+        if (min(it.s.lk - 1, tl.lim) < (j + 1) * kPrRows - 1) {
           const int last = lim - j * kPrRows;
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -533,7 +636,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // comes out above 2^8 (or there is no reference yet) does the true maximum
         // of the rows matter: it is taken, l and O are rescaled, and the weights are
         // computed again.  S stays in tensor memory until then.
-        for (bool renew = j == 0;;) {
+        for (bool renew = j == j0;;) {
           if (renew) {
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
@@ -550,7 +653,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             const float al = mn == -INFINITY ? 1.f : pr_ex2((m - mn) * c);
             m = mn;
             l *= al;
-            if (j > 0) {
+            if (j > j0) {
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 float o[32];
@@ -598,37 +701,33 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (lane == 0) mbar_arrive(p_full(t));
       }
       // ---- out = O / l
-      const bool keeps = row < tl.rows;
-      ACT* dst = static_cast<ACT*>(a.out) + (size_t)(tl.q0 + row) * a.out_stride + (size_t)tl.head * D;
-      if (tl.n > 0) {
+      ahead();
+      if (n > j0) {
         if (!dead) dead = !mbar_wait(o_full(t), oph, a.status);
         dead = __any_sync(0xffffffffu, dead);
         oph ^= 1;
-        if (dead) continue;
-        tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const bool none = lim < 0;  // O holds the products of zero weights: nothing to divide
-        // through shared memory, so that a store instruction writes whole 128-byte runs
-        // (stored row by row a lane, the epilogue took 5500 cycles of an item)
+        if (!dead) tc_fence_after();
+      }
+      const int r_here = tl.rows - 32 * (warp & 3);
+      // Rows of this warp, 64 channels at a time, through shared memory: a store
+      // instruction then writes whole 128-byte runs (a row a lane, the epilogue took
+      // 5500 cycles of an item).  begin(h, both) starts loading channels 64 h .. of the
+      // lane's row, get(h, q, o) completes 32 of them.
+      auto store_rows = [&](auto&& begin, auto&& get) {
         const uint32_t out = base + SM::OUT + (uint32_t)warp * 4096u;
-        const int r_here = tl.rows - 32 * (warp & 3);
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h) {
           float both[2][32];
-          tmem_ld32_nowait(to + (uint32_t)(64 * h), both[0]);
-          tmem_ld32_nowait(to + (uint32_t)(64 * h + 32), both[1]);
+          begin(h, both);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             float* o = both[q];
-            tmem_wait_ld32(o);
+            get(h, q, o);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = none ? 0u : Act<ACT>::pack2(o[8 * x + 2 * y] * inv, o[8 * x + 2 * y + 1] * inv);
-              sts_u128(out + (uint32_t)(lane * 128 + (((4 * q + x) ^ (lane & 7)) << 4)), make_uint4(w[0], w[1], w[2], w[3]));
-            }
+            for (int x = 0; x < 4; ++x)
+              sts_u128(out + (uint32_t)(lane * 128 + (((4 * q + x) ^ (lane & 7)) << 4)),
+                       make_uint4(Act<ACT>::pack2(o[8 * x], o[8 * x + 1]), Act<ACT>::pack2(o[8 * x + 2], o[8 * x + 3]),
+                                  Act<ACT>::pack2(o[8 * x + 4], o[8 * x + 5]), Act<ACT>::pack2(o[8 * x + 6], o[8 * x + 7])));
           }
           __syncwarp();
           ACT* to_row = static_cast<ACT*>(a.out) + (size_t)(tl.q0 + 32 * (warp & 3)) * a.out_stride + (size_t)tl.head * D +
@@ -641,12 +740,104 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           __syncwarp();
         }
-        tc_fence_before();
-      } else if (keeps) {
+      };
+      // 1 / l; zero for a row that sees no key (its O holds products of zero weights, and
+      // those are not numbers where a value is not)
+      auto inverse = [&](float l_all) { return l_all > 0.f ? 1.f / l_all : (l_all == 0.f ? 0.f : l_all); };
+      const bool none = lim < 0 || n == 0;
+      if (LISTED || (j0 == 0 && j1 >= it.n)) {  // the whole item
+        if (dead) return;
+        const float inv = inverse(l);
+        store_rows(
+            [&](int h, float(*both)[32]) {  // (without blocks: what was there before, not used)
+              tmem_ld32_nowait(to + (uint32_t)(64 * h), both[0]);
+              tmem_ld32_nowait(to + (uint32_t)(64 * h + 32), both[1]);
+            },
+            [&](int, int, float* o) {
+              tmem_wait_ld32(o);
 #pragma unroll
-        for (int x = 0; x < D; x += 8) *reinterpret_cast<uint4*>(dst + x) = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = 0; x < 32; ++x) o[x] = none ? 0.f : o[x] * inv;
+            });
+        tc_fence_before();
+        return;
       }
-    }
+      // ---- a part: leave it in the workspace; the last CTA to arrive joins them in order
+      if constexpr (!LISTED) {
+      using Part = PromptPart<D>;
+      int first;
+      const int n_parts = prompt_parts(it.u0, it.n, plan, &first);
+      auto part_o = [&](int k) {  // of the k-th CTA
+        return parts + ((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * Part::BYTES + (size_t)t * Part::O;
+      };
+      auto part_ml = [&](int k) {
+        return parts + ((size_t)(first + k) * 2 + (k == 0 ? 1 : 0)) * Part::BYTES + 2 * Part::O + (size_t)t * kPrRows * 8;
+      };
+      const int mine = (int)blockIdx.x - first;
+      {
+        float4* po = reinterpret_cast<float4*>(part_o(mine));
+        if (n > j0 && !dead) {  // (a warp that gave up still meets the others below)
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            float o[32];
+            tmem_ld32_nowait(to + (uint32_t)(32 * q), o);
+            tmem_wait_ld32(o);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              po[(8 * q + x) * kPrRows + row] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+        reinterpret_cast<float2*>(part_ml(mine))[row] = make_float2(m, l);
+      }
+      tc_fence_before();
+      __threadfence();
+      named_bar_sync(1 + t, 128);
+      if (row == 0) {
+        int* count = counters + 2 * first + t;
+        s_last[t] = atomic_add_acq_rel_gpu(count, 1) == n_parts - 1;
+        if (s_last[t]) *count = 0;
+      }
+      named_bar_sync(1 + t, 128);
+      if (!s_last[t]) return;
+      float M = -INFINITY, L = 0.f;
+      auto ml = [&](int k) {
+        const float* p = reinterpret_cast<const float*>(part_ml(k)) + 2 * row;
+        return make_float2(ld_cg(p), ld_cg(p + 1));
+      };
+      for (int k = 0; k < n_parts; ++k) M = fmaxf(M, ml(k).x);
+      auto weight = [&](const float2& x) { return x.x == -INFINITY ? (x.y == 0.f ? 0.f : x.y) : pr_ex2((x.x - M) * c); };
+      for (int k = 0; k < n_parts; ++k) {
+        const float2 x = ml(k);
+        L += weight(x) * x.y;
+      }
+      const float inv = inverse(L);
+      store_rows(
+          [&](int h, float(*both)[32]) {
+            float* o = both[0];  // 64 channels
+#pragma unroll
+            for (int x = 0; x < 64; ++x) o[x] = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < n_parts; ++k) {
+              const float w = weight(ml(k));
+              if (w == 0.f) continue;  // (a part that this tile had no block of holds no O)
+              const float* po = reinterpret_cast<const float*>(part_o(k)) + ((size_t)(16 * h) * kPrRows + row) * 4;
+              float4 v[16];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) v[x] = ld_cg4(po + (size_t)x * kPrRows * 4);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                o[4 * x] = fmaf(w, v[x].x, o[4 * x]);
+                o[4 * x + 1] = fmaf(w, v[x].y, o[4 * x + 1]);
+                o[4 * x + 2] = fmaf(w, v[x].z, o[4 * x + 2]);
+                o[4 * x + 3] = fmaf(w, v[x].w, o[4 * x + 3]);
+              }
+            }
+          },
+          [&](int, int, float* o) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = none ? 0.f : o[x] * inv;
+          });
+      }
+    });
   }
   tc_fence_before();
   __syncthreads();
@@ -655,23 +846,39 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 }
 
 static bool pairs_heads(int heads, int kv_heads) { return (heads / kv_heads) % 2 == 0; }
-// List entries that q_tokens queries of `batch` sequences can make, either way of pairing tiles.
+
+// Whether a call has so many items that whole ones, longest first, fill the CTAs
+// evenly (the split of items costs a CTA two stores of partial sums and a join).
+// Measured: nine prompts, 2144 items: listed 254 us, shared out 283; one prompt on
+// top of cached keys, 36 items: listed 43 us, shared out 31.
+static bool prompt_lists(int heads, int kv_heads, int tokens, int num_sms) {
+  const long long items = pairs_heads(heads, kv_heads) ? (long long)(tokens / kPrRows) * (heads / 2)
+                                                       : (long long)(tokens / (2 * kPrRows)) * heads;
+  return items >= 6LL * num_sms;
+}
+// List entries that `tokens` queries of `batch` sequences can make, either way of pairing tiles.
 static size_t prompt_most(int batch, int tokens) { return (size_t)tokens / kPrRows + (size_t)batch + 1; }
 
-size_t prompt_attention_ws_bytes(int, int batch, int tokens) {
-  return 256 + sizeof(PromptList) + ((prompt_most(batch, tokens) * sizeof(PromptItem) + 255) & ~(size_t)255);
+// Status word; then two counters a CTA and two parts a CTA (the larger head
+// size's), or the list.
+static size_t prompt_parts_at(int num_sms) { return 256 + (((size_t)num_sms * 8 + 255) & ~(size_t)255); }
+size_t prompt_attention_ws_bytes(int batch, int tokens, int num_sms) {
+  const size_t listed = prompt_parts_at(num_sms) + sizeof(PromptList) + prompt_most(batch, tokens) * sizeof(PromptEntry);
+  const size_t split = prompt_parts_at(num_sms) + (size_t)num_sms * 2 * PromptPart<128>::BYTES;
+  return ((listed > split ? listed : split) + 255) & ~(size_t)255;
 }
 
 template <typename ACT, int D>
-static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st) {
-  const auto kernel = prompt_attention_kernel<ACT, D>;
-  static std::atomic<unsigned long long> ready{0};  // devices on which the limit is raised
+static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st, int* kernels) {
+  static std::atomic<unsigned long long> ready{0};  // devices on which the limits are raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!((ready.load(std::memory_order_relaxed) >> (dev & 63)) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<D>::TOTAL);
-    if (e != cudaSuccess) return e;
+    for (const auto k : {prompt_attention_kernel<ACT, D, false>, prompt_attention_kernel<ACT, D, true>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<D>::TOTAL);
+      if (e != cudaSuccess) return e;
+    }
     ready.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
   }
   alignas(64) CUtensorMap m[3];
@@ -682,34 +889,41 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
       !encode_packed_map(&m[1], kp, nk, a.k_tokens > 0 ? a.k_stride : a.q_stride, a.kv_heads * D, kPrRows, D) ||
       !encode_packed_map(&m[2], vp, nk, a.k_tokens > 0 ? a.v_stride : a.q_stride, a.kv_heads * D, kPrRows, D))
     return cudaErrorInvalidValue;
-  PromptList* list = reinterpret_cast<PromptList*>(static_cast<char*>(ws) + 256);
-  PromptItem* items = reinterpret_cast<PromptItem*>(list + 1);
-  const int pair = pairs_heads(a.heads, a.kv_heads);
-  const int most = (int)prompt_most(a.batch, a.q_tokens);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(1024);
   cfg.stream = st;
-  e = cudaLaunchKernelEx(&cfg, prompt_list_kernel, a, pair ? kPrRows : 2 * kPrRows, list, items, most);
-  if (e != cudaSuccess) return e;
-  const long long ctas = (long long)most * (pair ? a.heads / 2 : a.heads);
-  if (ctas + 2LL * num_sms >= 2147483647LL) return cudaErrorInvalidValue;  // (refused by the entry point)
-  cfg.gridDim = dim3((unsigned)(ctas < num_sms ? ctas : num_sms));
+  const int pair = pairs_heads(a.heads, a.kv_heads);
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  PromptList* list = nullptr;
+  *kernels = 1;
+  if (prompt_lists(a.heads, a.kv_heads, a.q_tokens, num_sms)) {
+    const long long most = (long long)prompt_most(a.batch, a.q_tokens);
+    if (most * (pair ? a.heads / 2 : a.heads) + 2LL * num_sms >= 2147483647LL) return cudaErrorInvalidValue;  // (refused before)
+    list = reinterpret_cast<PromptList*>(base + prompt_parts_at(num_sms));
+    *kernels = 2;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    e = cudaLaunchKernelEx(&cfg, prompt_list_kernel, a, pair ? kPrRows : 2 * kPrRows, list,
+                           reinterpret_cast<PromptEntry*>(list + 1), (int)most);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3((unsigned)num_sms);
   cfg.blockDim = dim3(kPrThreads);
   cfg.dynamicSmemBytes = PromptSmem<D>::TOTAL;
-  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], a, (const PromptList*)list, (const PromptItem*)items, pair);
+  return cudaLaunchKernelEx(&cfg, list != nullptr ? prompt_attention_kernel<ACT, D, true> : prompt_attention_kernel<ACT, D, false>,
+                            m[0], m[1], m[2], a, pair, (const PromptList*)list, reinterpret_cast<int*>(base + 256),
+                            base + prompt_parts_at(num_sms));
 }
 
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st) {
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st, int* kernels) {
   if (a.act == ActKind::F16)
-    return a.head_dim == 64 ? prompt_launch<__half, 64>(a, ws, num_sms, st) : prompt_launch<__half, 128>(a, ws, num_sms, st);
-  return a.head_dim == 64 ? prompt_launch<__nv_bfloat16, 64>(a, ws, num_sms, st)
-                          : prompt_launch<__nv_bfloat16, 128>(a, ws, num_sms, st);
+    return a.head_dim == 64 ? prompt_launch<__half, 64>(a, ws, num_sms, st, kernels) : prompt_launch<__half, 128>(a, ws, num_sms, st, kernels);
+  return a.head_dim == 64 ? prompt_launch<__nv_bfloat16, 64>(a, ws, num_sms, st, kernels)
+                          : prompt_launch<__nv_bfloat16, 128>(a, ws, num_sms, st, kernels);
 }
 
 }  // namespace ds
