@@ -431,8 +431,9 @@ DS_API ds_status ds_tp_finish(ds_tp_layer* layer, const float* y, void* x_out, i
  * Every entry point returns DS_ERR_INVALID_ARG before any launch for pointers
  * that are not memory of the current device.  tokens == 0 is valid: nothing
  * is launched.  A workspace serves one call at a time: calls that may overlap
- * (two streams, two replayed graphs) need one each.  All four calls can be
- * captured into a CUDA graph. */
+ * (two streams, two replayed graphs) need one each.  One workspace, zero-filled
+ * once, serves any of these four calls in turn (not calls declared elsewhere in
+ * this header).  All can be captured into a CUDA graph. */
 typedef struct {
   void *k, *v;        /* DEVICE pages [num_pages][kv_heads][page_size][head_dim] in act_dtype;
                        * DS_U4: codes [num_pages][kv_heads][page_size][head_dim / 2], channel 2i
@@ -525,6 +526,30 @@ DS_API ds_status ds_prompt_attention(const void* q, const void* k, const void* v
                                      int64_t v_stride, int64_t out_stride, int q_tokens, int k_tokens,
                                      const int32_t* cu_q, const int32_t* cu_k, int batch, float scale,
                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* One layer over a paged cache: the regions of ds_layer_forward, with region 2
+ * as ds_paged_append and the attention over pages or packed prompts.  x_in,
+ * x_out [tokens][H]; the cache's kv_heads, head_dim and act_dtype are the
+ * layer's (heads, H / heads, act_dtype); rotary may be null.
+ *   new_tokens 0: whole prompts, packed by cu_seqlens (past_len is ignored: the
+ *                 first position of a sequence is 0); rows behind the last
+ *                 sequence give rows of x_out that mean nothing
+ *   1 .. 16:      tokens = batch * new_tokens rows (b, t) at positions
+ *                 past_len[b] + t (cu_seqlens is ignored; past_len not
+ *                 advanced); a slot with past_len[b] + new_tokens <= 0 is idle,
+ *                 its rows of x_out mean nothing
+ * Attention reads keys and values as the pages hold them, in prompts too; q,
+ * and k and v before the rotation, are rounded to the activation dtype once
+ * more than in ds_layer_forward.  tokens up to the layer's rows (1 .. 4096; see
+ * above).  The workspace need not be zero-filled but for its first 256 bytes
+ * (the status word).  Kernels per layer: those of ds_layer_forward and 2 to 4
+ * more. */
+DS_API size_t ds_layer_paged_workspace_bytes(const ds_layer* layer, const ds_paged_cache* cache, int tokens, int batch,
+                                             int new_tokens);
+DS_API ds_status ds_layer_forward_paged(ds_layer* layer, const void* x_in, void* x_out, int tokens,
+                                        const ds_paged_cache* cache, const ds_rotary* rotary,
+                                        const int32_t* cu_seqlens, const int32_t* past_len, int batch, int new_tokens,
+                                        void* workspace, size_t ws_bytes, void* stream);
 
 /* Device-side status flags recorded in the workspace. */
 #define DS_DEVFLAG_CACHE_OVERFLOW 0x1  /* past_len[b] + T > max_len for some row */

@@ -33,6 +33,7 @@
 
 #include "ds_layer.h"
 #include "internal.h"
+#include "paged.h"
 
 using namespace ds;
 
@@ -364,11 +365,54 @@ struct LayerIO {
   bool out_is_caller;  // x_out is the caller's buffer
 };
 
+// Region 2 over a paged cache: what enqueue_layer launches in place of the
+// attention over contiguous caches.  The QKV region has written q (fp32) and k,
+// v as packed rows (caches of one position a row).
+struct PagedStep {
+  PagedAppendArgs append;   // k, v: the packed rows; q_out: rotated q
+  PagedGatherArgs gather;   // prompts: the rows as the pages hold them, over k and v
+  PagedAttnArgs step;       // new tokens over the pages, or
+  PromptAttnArgs prompt;    // whole prompts
+  bool is_prompt = false;
+  void* attn_ws = nullptr;  // status word, counters, partial sums of the attention
+  void* o = nullptr;        // streaming path: the attention's output, widened to fp32 after it
+  int sms = 0;
+};
+
+// Kernels: narrow, append, (gather,) attention, (list,) (widen).
+cudaError_t enqueue_paged(const PagedStep& p, ActKind ak, const float* q, void* out_act, void* out_lo, float* out_f32,
+                          cudaStream_t st, int* kernels) {
+  const long long n = (long long)p.append.tokens * p.append.heads * p.append.c.head_dim;
+  cudaError_t e = launch_narrow(ak, q, p.append.q_out, n, st);
+  if (e == cudaSuccess) e = launch_paged_append(p.append, p.sms, st);
+  if (e != cudaSuccess) return e;
+  int attn = 1;
+  void* out = out_act != nullptr ? out_act : p.o;
+  if (p.is_prompt) {
+    if ((e = launch_paged_gather(p.gather, p.sms, st)) != cudaSuccess) return e;
+    PromptAttnArgs a = p.prompt;
+    a.out = out;
+    if ((e = launch_prompt_attention(a, p.attn_ws, p.sms, st, &attn)) != cudaSuccess) return e;
+  } else {
+    PagedAttnArgs a = p.step;
+    a.out = out;
+    if ((e = launch_paged_attention(a, p.attn_ws, p.sms, st)) != cudaSuccess) return e;
+  }
+  *kernels += 2 + attn + (p.is_prompt ? 1 : 0);
+  if (out_act == nullptr) {
+    *kernels += 1;
+    return launch_widen(ak, out, out_f32, n, st);
+  }
+  // (the output is in the activation type: nothing is left for the operand's low part)
+  return out_lo != nullptr ? cudaMemsetAsync(out_lo, 0, (size_t)n * 2, st) : cudaSuccess;
+}
+
 // Enqueues the region kernels of one layer.
 cudaError_t enqueue_layer(const ds_layer& L, const Plans& P, const Bufs& bf, const XMaps* xm, const LayerIO& io,
                           int B, int T, void* kc, void* vc, int max_len, const int32_t* past_len,
                           const float* stats_in, float* stats_out, int32_t* seq_inc, const ds_layer* next,
-                          bool first, cudaStream_t st, bool pdl, EventSink* es, std::vector<PatchNode>* rec) {
+                          bool first, cudaStream_t st, bool pdl, EventSink* es, std::vector<PatchNode>* rec,
+                          const PagedStep* paged = nullptr, int* paged_kernels = nullptr) {
   const ds_layer_config& c = L.cfg;
   const int H = c.hidden, F = c.ffn, nh = c.heads, d = H / nh, M = B * T;
   const WKind wk = wkind(c.weight_dtype);
@@ -394,6 +438,7 @@ cudaError_t enqueue_layer(const ds_layer& L, const Plans& P, const Bufs& bf, con
   ra.status = bf.status;
   // prompt chunks: tiled flash attention; decode and short chunks: split-KV
   auto launch_attn = [&](const AttnArgs& x) {
+    if (paged != nullptr) return enqueue_paged(*paged, ak, x.q, x.out_hi, x.out_lo, x.out, st, paged_kernels);
     return T >= kPrefillMinTokens ? launch_attention_prefill(ak, x, st, pdl) : launch_attention(ak, x, st, pdl);
   };
 
@@ -898,6 +943,173 @@ ds_status ds_layer_forward(ds_layer* layer, const void* x_in, void* x_out, int b
   if (s != DS_OK) return s;
   return layer_forward_enqueue(layer, x_in, x_out, batch, new_tokens, k_cache, v_cache, max_len, past_len, workspace,
                                stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of ds_layer_forward_paged: status word and the attention's counters
+// and partial sums, the layer's own regions, then the packed rows.
+struct PagedLayerWs {
+  size_t layer, zeros, q, k, v, o, total;
+  WsLayout wl;
+  Plans plans;
+};
+bool paged_layer_ws(const ds_layer& L, const PagedView& c, int tokens, int batch, int new_tokens, PagedLayerWs* w) {
+  if (!make_plans(L, tokens, &w->plans)) return false;
+  w->wl = ws_layout(L, tokens, 1, w->plans);
+  const size_t attn = new_tokens > 0 ? paged_attention_ws_bytes(c, L.cfg.heads, batch, new_tokens, L.sms)
+                                     : prompt_attention_ws_bytes(batch, tokens, L.sms);
+  const size_t rows = up256((size_t)tokens * L.cfg.hidden * 2);
+  size_t off = up256(attn);
+  auto take = [&](size_t n) {
+    const size_t o = off;
+    off += up256(n);
+    return o;
+  };
+  w->layer = take(w->wl.total);
+  w->zeros = take((size_t)std::max(tokens, batch) * 4);
+  w->q = take(rows);
+  w->k = take(rows);
+  w->v = take(rows);
+  w->o = take(rows);
+  w->total = off;
+  return true;
+}
+
+ds_status paged_layer_check(const ds_layer* layer, const ds_paged_cache* cache, int tokens, int batch, int new_tokens) {
+  if (layer == nullptr) return fail(DS_ERR_INVALID_ARG, "layer is null");
+  const ds_status s = paged_check_cache(cache, -1);
+  if (s != DS_OK) return s;
+  const ds_layer_config& c = layer->cfg;
+  if (cache->kv_heads != c.heads || cache->head_dim != c.hidden / c.heads || cache->act_dtype != c.act_dtype)
+    return fail(DS_ERR_INVALID_ARG, "the cache's kv_heads, head_dim and act_dtype must be the layer's");
+  if (batch < 1 || batch > 65535 || new_tokens < 0 || new_tokens > 16)
+    return fail(DS_ERR_INVALID_ARG, "batch must be in 1 .. 65535, new_tokens in 0 (prompts) .. 16");
+  if (new_tokens > 0 && (long long)batch * new_tokens != tokens)
+    return fail(DS_ERR_INVALID_ARG, "tokens must be batch * new_tokens");
+  if (tokens < 1 || tokens > layer->max_rows())
+    return fail(DS_ERR_UNSUPPORTED, "tokens out of the layer's range of rows");
+  return DS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ds_layer_paged_workspace_bytes(const ds_layer* layer, const ds_paged_cache* cache, int tokens, int batch,
+                                      int new_tokens) {
+  if (paged_layer_check(layer, cache, tokens, batch, new_tokens) != DS_OK) return 0;
+  PagedLayerWs w;
+  return paged_layer_ws(*layer, paged_view(cache), tokens, batch, new_tokens, &w) ? w.total : 0;
+}
+
+ds_status ds_layer_forward_paged(ds_layer* layer, const void* x_in, void* x_out, int tokens,
+                                 const ds_paged_cache* cache, const ds_rotary* rotary, const int32_t* cu_seqlens,
+                                 const int32_t* past_len, int batch, int new_tokens, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  ds_status s = paged_layer_check(layer, cache, tokens, batch, new_tokens);
+  if (s != DS_OK) return s;
+  if (!aligned16(x_in) || !aligned16(x_out) || x_in == x_out)
+    return fail(DS_ERR_INVALID_ARG, "x_in / x_out must be non-null, 16-byte aligned and not alias");
+  const int32_t* lens = new_tokens > 0 ? past_len : cu_seqlens;
+  if (lens == nullptr || (reinterpret_cast<uintptr_t>(lens) & 3u) != 0)
+    return fail(DS_ERR_INVALID_ARG, "past_len (new tokens) / cu_seqlens (prompts) must be a non-null int32 device array");
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(DS_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  if ((s = check_device(*layer)) != DS_OK) return s;
+  if ((s = paged_check_cache(cache, layer->device)) != DS_OK) return s;
+  if (rotary != nullptr && (s = paged_check_rotary(rotary, cache->head_dim, layer->device)) != DS_OK) return s;
+  for (const void* p : {x_in, (const void*)x_out, (const void*)lens, (const void*)workspace})
+    if (!paged_on_device(p, layer->device)) return fail(DS_ERR_INVALID_ARG, "a pointer is not memory of the current device");
+  const ds_layer& L = *layer;
+  const PagedView view = paged_view(cache);
+  PagedLayerWs w;
+  if (!paged_layer_ws(L, view, tokens, batch, new_tokens, &w)) return fail(DS_ERR_UNSUPPORTED, "no GEMM work split for this shape");
+  if (ws_bytes < w.total) return fail(DS_ERR_WORKSPACE, "workspace smaller than ds_layer_paged_workspace_bytes()");
+  char* base = static_cast<char*>(workspace);
+  unsigned* status = reinterpret_cast<unsigned*>(base);
+  Bufs bf = bufs_of(base + w.layer, w.wl);
+  bf.status = status;
+  XMaps xm;
+  if (w.plans.tile && !make_xmaps(L, w.plans, bf, tokens, &xm))
+    return fail(DS_ERR_CUDA, "cuTensorMapEncodeTiled failed for an activation operand");
+  const int H = L.cfg.hidden, nh = L.cfg.heads, d = H / nh;
+  int32_t* zeros = reinterpret_cast<int32_t*>(base + w.zeros);
+  PagedStep p;
+  p.is_prompt = new_tokens == 0;
+  p.attn_ws = base;
+  p.o = base + w.o;
+  p.sms = L.sms;
+  p.append.c = view;
+  if (rotary != nullptr) {
+    p.append.cos_sin = rotary->cos_sin;
+    p.append.max_pos = rotary->max_pos;
+    p.append.rotary_dim = rotary->rotary_dim;
+    p.append.interleaved = rotary->interleaved;
+  }
+  p.append.q = p.append.q_out = base + w.q;
+  p.append.k = base + w.k;
+  p.append.v = base + w.v;
+  p.append.q_stride = p.append.q_out_stride = p.append.k_stride = p.append.v_stride = H;
+  p.append.heads = nh;
+  p.append.tokens = tokens;
+  p.append.batch = batch;
+  p.append.cu = p.is_prompt ? cu_seqlens : nullptr;
+  p.append.T = p.is_prompt ? 1 : new_tokens;
+  p.append.past = p.is_prompt ? zeros : past_len;
+  p.append.status = status;
+  const float scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
+  if (p.is_prompt) {
+    p.gather.c = view;
+    p.gather.k = base + w.k;
+    p.gather.v = base + w.v;
+    p.gather.k_stride = p.gather.v_stride = H;
+    p.gather.tokens = tokens;
+    p.gather.batch = batch;
+    p.gather.cu = cu_seqlens;
+    p.gather.first = zeros;
+    p.gather.status = status;
+    PromptAttnArgs& a = p.prompt;
+    a.q = base + w.q;
+    a.k = base + w.k;
+    a.v = base + w.v;
+    a.heads = a.kv_heads = nh;
+    a.head_dim = d;
+    a.act = akind(L.cfg.act_dtype);
+    a.q_stride = a.k_stride = a.v_stride = a.out_stride = H;
+    a.q_tokens = a.k_tokens = tokens;
+    a.batch = batch;
+    a.cu_q = a.cu_k = cu_seqlens;
+    a.scale_log2 = scale_log2;
+    a.status = status;
+  } else {
+    PagedAttnArgs& a = p.step;
+    a.c = view;
+    a.q = base + w.q;
+    a.q_stride = a.out_stride = H;
+    a.heads = nh;
+    a.batch = batch;
+    a.T = new_tokens;
+    a.past = past_len;
+    a.scale_log2 = scale_log2;
+    a.status = status;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // counters (whatever ran in this workspace before), and the positions of the
+  // one-row caches that the QKV region writes
+  cudaError_t e = cudaMemsetAsync(base + kWsCounters, 0, kWsData - kWsCounters, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(base + w.layer, 0, w.wl.q, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(zeros, 0, w.q - w.zeros, st);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
+  const LayerIO io{x_in, x_out, false, false};
+  int extra = 0;
+  e = enqueue_layer(L, w.plans, bf, &xm, io, tokens, 1, base + w.k, base + w.v, 1, zeros, nullptr, nullptr, nullptr,
+                    nullptr, true, st, true, nullptr, nullptr, &p, &extra);
+  if (e != cudaSuccess) return cuda_fail(e, "region kernel launch (paged)");
+  g_launches += kernels_per_layer(w.plans) - 1 + extra;
+  return DS_OK;
 }
 
 ds_status ds_stack_create(ds_layer* const* layers, int n_layers, ds_stack** out) {

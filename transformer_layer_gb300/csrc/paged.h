@@ -21,6 +21,12 @@ struct PagedView {
   ActKind act = ActKind::F16;
 };
 
+// Workspace of the attention calls: status word, then counters (at a place of
+// their own, so that one workspace serves any of these calls in turn: every
+// call leaves them at zero), then partial sums.
+constexpr size_t kWsCounters = 256, kWsData = 256 + 4096;
+constexpr int kWsMaxCounters = 1024;
+
 struct PagedAppendArgs {
   PagedView c;
   const float* cos_sin = nullptr;  // null: no rotation
@@ -30,7 +36,8 @@ struct PagedAppendArgs {
   const void *k = nullptr, *v = nullptr;
   long long q_stride = 0, q_out_stride = 0, k_stride = 0, v_stride = 0;
   int heads = 0, tokens = 0, batch = 0;
-  const int32_t *cu = nullptr, *past = nullptr;
+  const int32_t *cu = nullptr, *past = nullptr;  // cu null: T rows a sequence
+  int T = 1;
   unsigned* status = nullptr;
 };
 
@@ -66,8 +73,17 @@ struct PromptAttnArgs {
   unsigned* status = nullptr;
 };
 
+// What of a paged cache is refused before any launch; `dev` -1: not its pointers.
+ds_status paged_check_cache(const ds_paged_cache* c, int dev);
+ds_status paged_check_rotary(const ds_rotary* r, int head_dim, int dev);
+PagedView paged_view(const ds_paged_cache* c);
+bool paged_on_device(const void* p, int dev);
+
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, int num_sms, cudaStream_t st);
+// n values (a multiple of 8) between fp32 and the activation type.
+cudaError_t launch_narrow(ActKind ak, const float* in, void* out, long long n, cudaStream_t st);
+cudaError_t launch_widen(ActKind ak, const void* in, float* out, long long n, cudaStream_t st);
 size_t paged_attention_ws_bytes(const PagedView& c, int heads, int batch, int T, int num_sms);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, int num_sms, cudaStream_t st);
 size_t prompt_attention_ws_bytes(int batch, int tokens, int num_sms);

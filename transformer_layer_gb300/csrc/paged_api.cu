@@ -106,6 +106,16 @@ PagedView view(const ds_paged_cache* c) {
   return v;
 }
 
+ds_status check_rotary(const ds_rotary* rotary, int d) {
+  if (!multiple_of(rotary->cos_sin, 16) || rotary->max_pos < 1)
+    return fail(DS_ERR_INVALID_ARG, "the rotation table must be non-null, 16-byte aligned, with max_pos >= 1");
+  if (rotary->rotary_dim < 16 || rotary->rotary_dim > d || rotary->rotary_dim % 16 != 0)
+    return fail(DS_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 up to head_dim");
+  if (rotary->interleaved != 0 && rotary->interleaved != 1)
+    return fail(DS_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  return DS_OK;
+}
+
 // A packed tensor's pointer and token stride.
 ds_status check_packed(const void* p, int64_t stride, int heads, int head_dim) {
   if (!multiple_of(p, 16)) return fail(DS_ERR_INVALID_ARG, "packed tensors must be non-null and 16-byte aligned");
@@ -131,6 +141,17 @@ ds_status check_batch(int tokens, int batch, const void* cu, const void* len) {
 float scale_log2(float scale) { return (float)((double)scale * 1.4426950408889634); }
 
 }  // namespace
+
+ds_status paged_check_cache(const ds_paged_cache* c, int dev) {
+  const ds_status s = check_cache(c);
+  return s != DS_OK || dev < 0 ? s : check_cache_device(c, dev);
+}
+ds_status paged_check_rotary(const ds_rotary* r, int head_dim, int dev) {
+  const ds_status s = check_rotary(r, head_dim);
+  return s != DS_OK || dev < 0 || on_device(r->cos_sin, dev) ? s : fail(DS_ERR_INVALID_ARG, kNotDevice);
+}
+PagedView paged_view(const ds_paged_cache* c) { return view(c); }
+bool paged_on_device(const void* p, int dev) { return on_device(p, dev); }
 }  // namespace ds
 
 using namespace ds;
@@ -161,14 +182,7 @@ ds_status ds_paged_append(const ds_paged_cache* cache, const ds_rotary* rotary, 
     if (q == q_out && q_stride != q_out_stride)
       return fail(DS_ERR_INVALID_ARG, "q rotated in place needs one stride");
   }
-  if (rotary != nullptr) {
-    if (!multiple_of(rotary->cos_sin, 16) || rotary->max_pos < 1)
-      return fail(DS_ERR_INVALID_ARG, "the rotation table must be non-null, 16-byte aligned, with max_pos >= 1");
-    if (rotary->rotary_dim < 16 || rotary->rotary_dim > d || rotary->rotary_dim % 16 != 0)
-      return fail(DS_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 up to head_dim");
-    if (rotary->interleaved != 0 && rotary->interleaved != 1)
-      return fail(DS_ERR_INVALID_ARG, "interleaved must be 0 or 1");
-  }
+  if (rotary != nullptr) DS_TRY(check_rotary(rotary, d));
   int dev = -1;
   const int sms = device_sms(&dev);
   if (sms == 0) return fail(DS_ERR_CUDA, "no CUDA device");

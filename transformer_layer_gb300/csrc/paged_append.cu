@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(kRowThreads, 5) paged_append_kernel(const Page
   int base = sub * iters * RPI;
   fetch(base);
 
-  const int b = find_sequence(a.cu, a.batch, t);
+  const int b = a.cu != nullptr ? find_sequence(a.cu, a.batch, t) : t / a.T;
   if (b >= a.batch) return;
-  const int pos = a.past[b] + (t - a.cu[b]);
+  const int pos = a.past[b] + (t - (a.cu != nullptr ? a.cu[b] : b * a.T));
   if (pos < 0) return;
   unsigned why = 0;
   const long long row0 = page_row(a.c, b, pos, &why);
@@ -360,6 +360,46 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, int num_sms, cudaStrea
     return a.c.head_dim == 64 ? append_launch<__half, 64>(a, num_sms, st) : append_launch<__half, 128>(a, num_sms, st);
   return a.c.head_dim == 64 ? append_launch<__nv_bfloat16, 64>(a, num_sms, st)
                             : append_launch<__nv_bfloat16, 128>(a, num_sms, st);
+}
+
+template <typename ACT, bool NARROW>
+__global__ void __launch_bounds__(256) convert_rows_kernel(const void* in, void* out, long long n8) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  float x[8];
+  if constexpr (NARROW) {
+    const float4* p = static_cast<const float4*>(in) + 2 * i;
+    const float4 a = p[0], b = p[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    static_cast<uint4*>(out)[i] = pack8<ACT>(x);
+  } else {
+    unpack8<ACT>(static_cast<const uint4*>(in)[i], x);
+    float4* p = static_cast<float4*>(out) + 2 * i;
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+template <bool NARROW>
+static cudaError_t convert_launch(ActKind ak, const void* in, void* out, long long n, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n / 8 + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return ak == ActKind::F16 ? cudaLaunchKernelEx(&cfg, convert_rows_kernel<__half, NARROW>, in, out, n / 8)
+                            : cudaLaunchKernelEx(&cfg, convert_rows_kernel<__nv_bfloat16, NARROW>, in, out, n / 8);
+}
+cudaError_t launch_narrow(ActKind ak, const float* in, void* out, long long n, cudaStream_t st) {
+  return convert_launch<true>(ak, in, out, n, st);
+}
+cudaError_t launch_widen(ActKind ak, const void* in, float* out, long long n, cudaStream_t st) {
+  return convert_launch<false>(ak, in, out, n, st);
 }
 
 template <typename ACT, int D>

@@ -155,7 +155,7 @@ struct PaPlan {
   int min_chunk = 4;    // blocks a CTA takes at least
   float* part_o = nullptr;   // [CTA][2][rows][D]
   float* part_ml = nullptr;  // [CTA][2][rows][2]
-  int* counters = nullptr;   // [segments], zero between calls
+  int* counters = nullptr;   // [CTA], zero between calls: of the segment that a later CTA continues
 };
 
 __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
@@ -669,7 +669,6 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
     const long long seg_hi = seg_lo + nb;
     const bool whole = seg_lo >= c_lo && seg_hi <= c_hi;
     const int part = blockIdx.x * 2 + (seg_lo < c_lo ? 0 : 1);
-    const int seg_id = b * per_b + seg;
     auto store = [&](int r, int c, float4 v) {  // row r of the segment, 4 channels at c
       const int rr = rt * RP + r;
       if (rr >= R) return;
@@ -707,10 +706,10 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
       const int first = (int)(seg_lo / chunk), last = (int)((seg_hi - 1) / chunk);
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomic_add_acq_rel_gpu(pl.counters + seg_id, 1) == last - first;
+      if (tid == 0) s_last = atomic_add_acq_rel_gpu(pl.counters + first, 1) == last - first;
       __syncthreads();
       if (s_last) {
-        if (tid == 0) pl.counters[seg_id] = 0;
+        if (tid == 0) pl.counters[first] = 0;
         for (int i = tid; i < RP * (D / 4); i += kPaThreads) {
           const int r = i / (D / 4), c = (i % (D / 4)) * 4;
           float M = -INFINITY, L = 0.f;
@@ -759,7 +758,7 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
 static int pa_rows(int heads, int kv_heads, int T) { return heads / kv_heads * T; }
 
 struct PaWs {
-  size_t counters, part_o, part_ml, total;
+  size_t part_o, part_ml, total;
   int nr, nrt, grid, min_chunk;
 };
 // Blocks of 16 positions a CTA takes at least: one 64-position tile a warp of
@@ -780,11 +779,11 @@ static PaWs pa_ws(const PagedView& c, int heads, int batch, int T, int num_sms) 
   w.min_chunk = pa_min_chunk(c);
   const long long most = (((long long)c.table_stride << c.page_shift) / 16) * batch * c.kv_heads * w.nrt;
   const long long ctas = (most + w.min_chunk - 1) / w.min_chunk;
-  const long long room = (long long)num_sms * pa_ctas(c.u4, w.nr);
+  long long room = (long long)num_sms * pa_ctas(c.u4, w.nr);
+  if (room > kWsMaxCounters) room = kWsMaxCounters;
   w.grid = (int)(ctas < room ? ctas : room);
   const size_t slots = (size_t)w.grid * 2 * 8 * w.nr;
-  w.counters = 256;
-  w.part_ml = w.counters + up((size_t)batch * c.kv_heads * w.nrt * 4);
+  w.part_ml = kWsData;
   w.part_o = w.part_ml + up(slots * 2 * 4);
   w.total = w.part_o + up(slots * c.head_dim * 4);
   return w;
@@ -836,7 +835,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* ws, int num_sms
   PaPlan pl;
   pl.nrt = w.nrt;
   pl.min_chunk = w.min_chunk;
-  pl.counters = reinterpret_cast<int*>(base + w.counters);
+  pl.counters = reinterpret_cast<int*>(base + kWsCounters);
   pl.part_ml = reinterpret_cast<float*>(base + w.part_ml);
   pl.part_o = reinterpret_cast<float*>(base + w.part_o);
   if (a.c.act == ActKind::F16)

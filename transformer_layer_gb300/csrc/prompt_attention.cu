@@ -859,12 +859,10 @@ static bool prompt_lists(int heads, int kv_heads, int tokens, int num_sms) {
 // List entries that `tokens` queries of `batch` sequences can make, either way of pairing tiles.
 static size_t prompt_most(int batch, int tokens) { return (size_t)tokens / kPrRows + (size_t)batch + 1; }
 
-// Status word; then two counters a CTA and two parts a CTA (the larger head
-// size's), or the list.
-static size_t prompt_parts_at(int num_sms) { return 256 + (((size_t)num_sms * 8 + 255) & ~(size_t)255); }
+// Two parts a CTA (the larger head size's), or the list, behind the counters.
 size_t prompt_attention_ws_bytes(int batch, int tokens, int num_sms) {
-  const size_t listed = prompt_parts_at(num_sms) + sizeof(PromptList) + prompt_most(batch, tokens) * sizeof(PromptEntry);
-  const size_t split = prompt_parts_at(num_sms) + (size_t)num_sms * 2 * PromptPart<128>::BYTES;
+  const size_t listed = kWsData + sizeof(PromptList) + prompt_most(batch, tokens) * sizeof(PromptEntry);
+  const size_t split = kWsData + (size_t)num_sms * 2 * PromptPart<128>::BYTES;
   return ((listed > split ? listed : split) + 255) & ~(size_t)255;
 }
 
@@ -897,13 +895,14 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
   cfg.numAttrs = 1;
   cfg.stream = st;
   const int pair = pairs_heads(a.heads, a.kv_heads);
+  if (2 * num_sms > kWsMaxCounters) num_sms = kWsMaxCounters / 2;
   unsigned char* base = static_cast<unsigned char*>(ws);
   PromptList* list = nullptr;
   *kernels = 1;
   if (prompt_lists(a.heads, a.kv_heads, a.q_tokens, num_sms)) {
     const long long most = (long long)prompt_most(a.batch, a.q_tokens);
     if (most * (pair ? a.heads / 2 : a.heads) + 2LL * num_sms >= 2147483647LL) return cudaErrorInvalidValue;  // (refused before)
-    list = reinterpret_cast<PromptList*>(base + prompt_parts_at(num_sms));
+    list = reinterpret_cast<PromptList*>(base + kWsData);
     *kernels = 2;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(1024);
@@ -915,8 +914,8 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
   cfg.blockDim = dim3(kPrThreads);
   cfg.dynamicSmemBytes = PromptSmem<D>::TOTAL;
   return cudaLaunchKernelEx(&cfg, list != nullptr ? prompt_attention_kernel<ACT, D, true> : prompt_attention_kernel<ACT, D, false>,
-                            m[0], m[1], m[2], a, pair, (const PromptList*)list, reinterpret_cast<int*>(base + 256),
-                            base + prompt_parts_at(num_sms));
+                            m[0], m[1], m[2], a, pair, (const PromptList*)list, reinterpret_cast<int*>(base + kWsCounters),
+                            base + kWsData);
 }
 
 cudaError_t launch_prompt_attention(const PromptAttnArgs& a, void* ws, int num_sms, cudaStream_t st, int* kernels) {

@@ -68,6 +68,9 @@ _SIGS = {
     "ds_paged_attention_workspace_bytes": (C.c_size_t, [_vp, C.c_int, C.c_int, C.c_int]),
     "ds_paged_attention": (C.c_int, [_vp, _vp, _vp, C.c_int, C.c_int64, C.c_int64, _vp, C.c_int, C.c_int, C.c_float,
                                      _vp, C.c_size_t, _vp]),
+    "ds_layer_paged_workspace_bytes": (C.c_size_t, [_vp, _vp, C.c_int, C.c_int, C.c_int]),
+    "ds_layer_forward_paged": (C.c_int, [_vp, _vp, _vp, C.c_int, _vp, _vp, _vp, _vp, C.c_int, C.c_int, _vp, C.c_size_t,
+                                         _vp]),
     "ds_prompt_attention_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
     "ds_prompt_attention": (C.c_int, [_vp, _vp, _vp, _vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int64, C.c_int64,
                                       C.c_int64, C.c_int64, C.c_int, C.c_int, _vp, _vp, C.c_int, C.c_float, _vp,
@@ -563,6 +566,25 @@ def ds_prompt_attention(q, k, v, out, cu_q, cu_k, batch, ws, ws_bytes, scale=Non
                                       _check_int32(cu_q, batch + 1, "cu_q"), _check_int32(cu_k, batch + 1, "cu_k"),
                                       batch, scale if scale is not None else d ** -0.5, ws.data_ptr(), ws_bytes,
                                       _raw_stream(stream)), "ds_prompt_attention")
+
+
+def ds_layer_paged_workspace_bytes(layer, cache, tokens, batch, new_tokens):
+    return int(load().ds_layer_paged_workspace_bytes(layer, C.byref(cache), tokens, batch, new_tokens))
+
+
+def ds_layer_forward_paged(layer, x_in, x_out, cache, rotary, cu_seqlens, past_len, batch, new_tokens, ws, ws_bytes,
+                           stream=None):
+    """x_in, x_out [tokens][H]; new_tokens 0: prompts packed by cu_seqlens
+    (past_len may be None), else cu_seqlens may be None; rotary may be None."""
+    for t, what in ((x_in, "x_in"), (x_out, "x_out")):
+        _check_like(t, (x_in.shape[0], None), cache.shape[2], what)
+    lens, n, what = (past_len, batch, "past_len") if new_tokens else (cu_seqlens, batch + 1, "cu_seqlens")
+    p = _check_int32(lens, n, what)
+    _check_batch(cache.shape[3], batch)
+    _check(load().ds_layer_forward_paged(layer, _ptr(x_in), _ptr(x_out), x_in.shape[0], C.byref(cache),
+                                         C.byref(rotary) if rotary is not None else None, None if new_tokens else p,
+                                         p if new_tokens else None, batch, new_tokens, _ptr(ws), ws_bytes,
+                                         _raw_stream(stream)), "ds_layer_forward_paged")
 
 
 def ds_launch_count():
