@@ -451,6 +451,16 @@ def test_prompt_attention(dtype, nh, nk, d, lq, lk):
     assert torch.equal(out[:n], again[:n])
 
 
+@pytest.mark.parametrize("dtype,nh,nk,d,lq,lk", [
+    (F16, 5, 5, 128, [600, 0, 300], [15000, 100, 12000]),
+    (BF16, 4, 2, 64, [130, 257], [75000, 60000]),
+])
+def test_prompt_chunks_over_more_keys_than_cache_memory_holds(dtype, nh, nk, d, lq, lk):
+    """Keys and values of more than 64 MB, few items: the tiles of a sequence walk them side by side."""
+    assert sum(lk) * nk * d * 4 > 64 << 20
+    test_prompt_attention(dtype, nh, nk, d, lq, lk)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_prompt_sequences_do_not_meet(dtype):
     """Values that are not finite stay in their own sequence, at every place of a tile."""

@@ -261,7 +261,7 @@ template <typename ACT, int D, bool LISTED>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                             const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptAttnArgs a,
-                            int pair_heads, const PromptList* list, int* counters, unsigned char* parts) {
+                            int pair_heads, int lanes, const PromptList* list, int* counters, unsigned char* parts) {
   using SM = PromptSmem<D>;
   constexpr int NST = SM::NST, TILE = SM::TILE;
   constexpr bool kBf16 = std::is_same<ACT, __nv_bfloat16>::value;
@@ -271,6 +271,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   __shared__ long long s_items[kPrThreads / 32];
   __shared__ int s_longest[kPrThreads / 32];
   __shared__ PromptBound s_bound[2];
+  __shared__ int4 s_lane[kPromptLanes];  // sequence, tile, blocks of the tile, of the sequence's last
+  __shared__ int s_plan[3];              // units of a share, its lane's first CTA, whether lanes are used
   __shared__ int s_last[2];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
@@ -344,6 +346,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       s_longest[warp] = longest;
     }
     if (tid < 2) s_bound[tid].b = a.batch;  // behind the last item
+    if (tid < 3) s_plan[tid] = 0;
     __syncthreads();
     long long before = inc - sum, total = 0, before_items = inc_items - sum_items, items = 0;
 #pragma unroll
@@ -357,12 +360,51 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       longest = max(longest, s_longest[w]);
     }
     plan = prompt_plan(total, items, gridDim.x, longest);
+    if (lanes && plan.cut && items <= (long long)kPromptLanes * hp) {
+      int at = (int)(before_items / hp);
+      for (int b = b0; b < b1; ++b) {
+        const PromptSeq s = seq_of(b);
+        const int T = prompt_tiles(s, unit);
+        for (int t = 0; t < T; ++t) s_lane[at++] = make_int4(b, t, prompt_blocks(s, unit, t), prompt_blocks(s, unit, T - 1));
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const int n_lanes = (int)(items / hp);
+        const int4 e = lane < n_lanes ? s_lane[lane] : make_int4(0, 0, 0, 0);
+        auto mine = [&](int c) { return lane < n_lanes ? prompt_lane_ctas(hp, e.w, c) : 0; };
+        int share = prompt_lane_share(total, n_lanes, gridDim.x, plan,
+                                      [&](int c) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)mine(c)); });
+        const int k = share > 0 ? mine(share) : 0, size = k > 0 ? prompt_lane_chunk(hp, e.z, k) : 0;
+        if (__any_sync(0xffffffffu, k > 0 && size < 2 * kPromptEdge)) share = 0;
+        int end = k;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += v;
+        }
+        const int c = (int)blockIdx.x - (end - k);  // this CTA, of the lane's
+        if (share > 0 && c >= 0 && c < k) {
+          s_plan[0] = size;
+          s_plan[1] = end - k;
+          for (int i = 0; i < 2; ++i)
+            if ((c + i) * size < hp * (e.z + kPromptItem))
+              s_bound[i] = prompt_lane_locate(plan, e.x, e.y, e.z, (long long)(c + i) * size);
+        }
+        if (lane == 0) s_plan[2] = share;
+      }
+      __syncthreads();
+      if (s_plan[2] > 0) {
+        plan.lanes = 1;
+        plan.chunk = s_plan[0];  // (a CTA behind the last lane has no share and no use for these)
+        plan.base = s_plan[1];
+      }
+    }
     if (plan.flat) {
       before = before_items;
       sum = sum_items;
     }
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 && !plan.lanes; ++i) {
       const long long u = ((long long)blockIdx.x + i) * plan.chunk;
       if (u < before || u >= before + sum) continue;
       long long at = before;
@@ -856,6 +898,11 @@ static bool prompt_lists(int heads, int kv_heads, int tokens, int num_sms) {
                                                        : (long long)(tokens / (2 * kPrRows)) * heads;
   return items >= 6LL * num_sms;
 }
+// Whether shares lie in lanes (prompt_split.h) where they can: keys and values beyond
+// half of L2 are then read from memory once, not once a tile.
+static bool prompt_lanes(const PromptAttnArgs& a) {
+  return (long long)a.k_tokens * a.kv_heads * a.head_dim * 4 > (64LL << 20);
+}
 // List entries that `tokens` queries of `batch` sequences can make, either way of pairing tiles.
 static size_t prompt_most(int batch, int tokens) { return (size_t)tokens / kPrRows + (size_t)batch + 1; }
 
@@ -914,7 +961,7 @@ static cudaError_t prompt_launch(const PromptAttnArgs& a, void* ws, int num_sms,
   cfg.blockDim = dim3(kPrThreads);
   cfg.dynamicSmemBytes = PromptSmem<D>::TOTAL;
   return cudaLaunchKernelEx(&cfg, list != nullptr ? prompt_attention_kernel<ACT, D, true> : prompt_attention_kernel<ACT, D, false>,
-                            m[0], m[1], m[2], a, pair, (const PromptList*)list, reinterpret_cast<int*>(base + kWsCounters),
+                            m[0], m[1], m[2], a, pair, (int)prompt_lanes(a), (const PromptList*)list, reinterpret_cast<int*>(base + kWsCounters),
                             base + kWsData);
 }
 

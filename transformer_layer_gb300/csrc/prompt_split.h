@@ -25,6 +25,7 @@ namespace ds {
 constexpr int kPromptEdge = 4;  // least blocks of a part
 constexpr int kPromptItem = 2;  // units of an item besides its blocks
 constexpr int kPromptParts = 8; // about as many parts as an item may be cut into
+constexpr int kPromptLanes = 32; // most lanes (a thread of a warp each)
 constexpr int kPromptJoin = 8;  // what a cut costs a CTA, in units: storing its parts, joining one
 
 struct PromptSeq {
@@ -58,6 +59,8 @@ struct PromptPlan {
   long long chunk = 1;  // units from one bound to the next
   int cut = 0;          // whether bounds may cut items
   int flat = 0;         // every item is one unit
+  int lanes = 0;        // shares lie in lanes: units are counted from the lane's start,
+  int base = 0;         // its first CTA
 };
 // An even share of `total` units.  Whole items make some CTA late by what the
 // longest is over that, or by half of it; they are cut where that costs more
@@ -78,6 +81,42 @@ DS_HD PromptPlan prompt_plan(long long total, long long items, int grid, int lon
     p.chunk = 1;
   }
   return p;
+}
+// Lanes: the least share for which they fit into `grid` CTAs, 0 where that is more
+// than a sixteenth above the even share or parts would be too short.  ctas(c) is
+// the number of CTAs that all lanes take at c units each.
+template <class F>
+DS_HD int prompt_lane_share(long long total, long long lanes, int grid, const PromptPlan& p, const F& ctas) {
+  if (!p.cut || lanes > kPromptLanes || lanes * 8 > grid || total >= (1LL << 30)) return 0;
+  int lo = (int)((total + grid - 1) / grid), hi = lo + lo / 16;
+  if (p.chunk > lo || ctas(hi) > grid) return 0;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ctas(mid) <= grid) hi = mid;
+    else lo = mid + 1;
+  }
+  return hi;
+}
+// CTAs of a lane whose sequence's last tile sees `top` blocks, at c units each.
+DS_HD int prompt_lane_ctas(int hp, int top, int c) { return (hp * (top + kPromptItem) + c - 1) / c; }
+
+// Units of each of a lane's k shares; lanes are not taken where that is below
+// 2 kPromptEdge for one of them.
+DS_HD int prompt_lane_chunk(int hp, int n, int k) { return (hp * (n + kPromptItem) + k - 1) / k; }
+
+// Block j of an item of n as a bound.
+DS_HD int prompt_edge(const PromptPlan& p, int j, int n) {
+  return !p.cut || j < kPromptEdge || n - j < kPromptEdge ? (2 * j < n || j < 1 ? 0 : n) : j;
+}
+// The bound at unit v of tile t's lane of sequence b.
+DS_HD PromptBound prompt_lane_locate(const PromptPlan& p, int b, int t, int n, long long v) {
+  PromptBound r;
+  r.b = b;
+  r.t = t;
+  r.h = (int)(v / (n + kPromptItem));
+  r.u0 = (long long)r.h * (n + kPromptItem);
+  r.j = prompt_edge(p, (int)(v - r.u0) - kPromptItem, n);
+  return r;
 }
 // The bound at unit v (0 <= v < the units of all heads) of sequence b, whose
 // first unit is `before`.
@@ -103,8 +142,7 @@ DS_HD PromptBound prompt_locate(const PromptSeq& s, int unit, const PromptPlan& 
   const int n = prompt_blocks(s, unit, lo);
   const long long first = prompt_units(s, unit, lo);
   r.u0 = before + r.h * per_head + first;
-  r.j = (int)(v - first) - kPromptItem;
-  if (!p.cut || r.j < kPromptEdge || n - r.j < kPromptEdge) r.j = 2 * r.j < n || r.j < 1 ? 0 : n;
+  r.j = prompt_edge(p, (int)(v - first) - kPromptItem, n);
   return r;
 }
 // The CTAs that hold parts of the item of n blocks at unit u0: *first and the
@@ -113,7 +151,7 @@ DS_HD int prompt_parts(long long u0, int n, const PromptPlan& p, int* first) {
   const long long chunk = p.chunk;
   const long long c_lo = (u0 + kPromptItem + kPromptEdge + chunk - 1) / chunk;
   const long long c_hi = (u0 + kPromptItem + n - kPromptEdge) / chunk;
-  *first = (int)(c_lo - 1);
+  *first = p.base + (int)(c_lo - 1);
   return p.cut && n >= 2 * kPromptEdge && c_hi >= c_lo ? (int)(c_hi - c_lo) + 2 : 1;
 }
 
@@ -126,6 +164,10 @@ struct PromptItem {
 template <class F>
 DS_HD PromptItem prompt_after(PromptItem x, const PromptPlan& p, int batch, int unit, int hp, const F& seq_of) {
   x.u0 += p.flat ? 1 : x.n + kPromptItem;
+  if (p.lanes) {
+    if (++x.h >= hp) x.b = batch;
+    return x;
+  }
   ++x.t;
   while (x.t >= prompt_tiles(x.s, unit)) {
     x.t = 0;
