@@ -408,8 +408,8 @@ DS_API ds_status ds_tp_finish(ds_tp_layer* layer, const float* y, void* x_out, i
  * Packed tensors hold the tokens of all sequences one after the other,
  * [tokens][heads][head_dim]: the rows of sequence b are cu[b] .. cu[b+1]-1,
  * with cu a DEVICE int32 array of batch + 1 non-decreasing entries, cu[0] = 0.
- * A sequence may have no rows.  Rows behind cu[batch] belong to nobody: they
- * are neither read nor written.  A packed tensor has a token stride in
+ * A sequence may have no rows.  Rows behind cu[batch] belong to nobody: what
+ * they hold reaches no result, and they are not written.  A packed tensor has a token stride in
  * elements (a multiple of 8, at least heads * head_dim), so that q, k and v
  * may be parts of one projection's rows; heads and channels are contiguous.
  *

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) paged_append_kernel(const Page
 
   const int b = a.cu != nullptr ? find_sequence(a.cu, a.batch, t) : t / a.T;
   if (b >= a.batch) return;
-  const int pos = a.past[b] + (t - (a.cu != nullptr ? a.cu[b] : b * a.T));
+  const int pos = min(a.past[b], 1 << 30) + (t - (a.cu != nullptr ? a.cu[b] : b * a.T));
   if (pos < 0) return;
   unsigned why = 0;
   const long long row0 = page_row(a.c, b, pos, &why);
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_gather_kernel(const PagedGa
   if (t >= a.tokens) return;
   const int b = find_sequence(a.cu, a.batch, t);
   if (b >= a.batch) return;
-  const int pos = a.first[b] + (t - a.cu[b]);
+  const int pos = min(a.first[b], 1 << 30) + (t - a.cu[b]);
   if (pos < 0) return;
   unsigned why = 0;
   const long long row0 = page_row(a.c, b, pos, &why);

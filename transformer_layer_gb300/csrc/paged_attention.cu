@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
     // ---- segment (b, kh, rt): blocks [k0, k1) are this CTA's
     const int kh = seg / pl.nrt, rt = seg - kh * pl.nrt;
     const int k0 = (int)(cur - seg_lo), k1 = (int)min((long long)nb, c_hi - seg_lo);
-    const int len = pa_len(a, b), past = a.past[b];
+    const int len = pa_len(a, b), past = min(a.past[b], a.c.table_stride << a.c.page_shift);
     const int ntile = (k1 - k0 + KB - 1) / KB;  // tiles; warp w takes w, w + kPaWarps, ...
     const int32_t* table = a.c.table + (size_t)b * a.c.table_stride;
 

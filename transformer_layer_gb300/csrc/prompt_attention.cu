@@ -899,7 +899,10 @@ static bool prompt_lists(int heads, int kv_heads, int tokens, int num_sms) {
   return items >= 6LL * num_sms;
 }
 // Whether shares lie in lanes (prompt_split.h) where they can: keys and values beyond
-// half of L2 are then read from memory once, not once a tile.
+// half of L2 are then read from memory about once, not once a tile.  Measured end to
+// end / in lanes: 42 MB 43.7 / 47.7 us, 107 MB 66.2 / 62.1, 136 MB 250 / 233; two
+// chunks of 384 to 701 queries over 6000 to 9700 keys, 40 heads, 328 MB: 174 / 163
+// (840 / 478 MB from memory).
 static bool prompt_lanes(const PromptAttnArgs& a) {
   return (long long)a.k_tokens * a.kv_heads * a.head_dim * 4 > (64LL << 20);
 }
