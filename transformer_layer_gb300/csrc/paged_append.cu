@@ -24,6 +24,11 @@
 // (A form with one chunk a lane, the partner by shuffle and true divisions in
 // the quantiser issued 221 instructions per two rows and ran at half the
 // bandwidth.)
+//
+// Measured: 24 prompts, 32 query and 8 key heads, 16-bit pages, appended and
+// read back: 63 us, 6.5 TB/s (98 % of a copy).  4-bit pages are bound by issue
+// (about 190 instructions per four rows, most of them the quantiser's): 7
+// prompts, 20 heads, 31 us, 3.6 TB/s.
 #include "paged.cuh"
 
 namespace ds {
@@ -103,6 +108,33 @@ struct RowLane {
   }
 };
 
+constexpr float kMagic = 12582912.f, kNear = 0.5f - 3.0e-5f;
+
+// The codes of a lane's channels, w, with those decided anew whose quotient lies
+// near a half (rare: out of line, so that its registers and code are not the common path's).
+struct RowLaneValues {
+  float x[16];
+};
+__device__ __noinline__ uint2 quantize_near_halves(RowLaneValues v, float mf, float sf, float inv, uint2 codes) {
+  uint32_t w[2] = {codes.x, codes.y};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float d = __fsub_rn(v.x[i], mf), t = __saturatef(d * inv);
+    const float r = __fsub_rn(fmaf(t, 15.f, kMagic), kMagic);
+    const float e = fmaf(t, 15.f, -r);
+    if (fabsf(e) > kNear) {
+      const float low = e > 0.f ? r : r - 1.f;  // the code below the half
+      const float rem = fmaf(-(low + 0.5f), sf, d);
+      float c = rem > 0.f ? low + 1.f : low;
+      if (rem == 0.f) c = rintf(low + 0.5f);
+      else if (fabsf(rem) < sf * 2e-6f) c = rintf(__fdiv_rn(d, sf));
+      const int sh = 4 * (i & 7);
+      w[i >> 3] = (w[i >> 3] & ~(15u << sh)) | ((uint32_t)c << sh);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // Quantises the row whose channels the LPR lanes of this lane's group hold, 16
 // each: the codes of its two chunks, and the row's (scale, minimum).
 // code = clamp(rne(d / s), 0, 15), d = x - m, by the reciprocal: t = d / (15 s),
@@ -131,7 +163,6 @@ __device__ __forceinline__ uint2 quantize_row(const float (&x)[16], __half2* sca
   const float sf = __half2float(s);
   const float inv = sf > 0.f ? __fdividef(1.f, sf * 15.f) : 0.f;
   *scale = __halves2half2(s, m);
-  constexpr float kMagic = 12582912.f;
   constexpr uint32_t kMagicBits = 0x4B400000u;  // its bits: their multiples of 16 wrap to a constant
   constexpr uint32_t kFix = kMagicBits * 0x11111111u;
   uint32_t w[2] = {0u, 0u};
@@ -145,29 +176,21 @@ __device__ __forceinline__ uint2 quantize_row(const float (&x)[16], __half2* sca
   }
   w[0] -= kFix;
   w[1] -= kFix;
-  constexpr float kNear = 0.5f - 3.0e-5f;
+  const uint2 codes = make_uint2(w[0], w[1]);
   if (far > kNear) {
+    RowLaneValues v;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float d = __fsub_rn(x[i], mf), t = __saturatef(d * inv);
-      const float r = __fsub_rn(fmaf(t, 15.f, kMagic), kMagic);
-      const float e = fmaf(t, 15.f, -r);
-      if (fabsf(e) > kNear) {
-        const float low = e > 0.f ? r : r - 1.f;  // the code below the half
-        const float rem = fmaf(-(low + 0.5f), sf, d);
-        float c = rem > 0.f ? low + 1.f : low;
-        if (rem == 0.f) c = rintf(low + 0.5f);
-        else if (fabsf(rem) < sf * 2e-6f) c = rintf(__fdiv_rn(d, sf));
-        const int sh = 4 * (i & 7);
-        w[i >> 3] = (w[i >> 3] & ~(15u << sh)) | ((uint32_t)c << sh);
-      }
-    }
+    for (int i = 0; i < 16; ++i) v.x[i] = x[i];
+    return quantize_near_halves(v, mf, sf, inv, codes);
   }
-  return make_uint2(w[0], w[1]);
+  return codes;
 }
 
+// Registers: 4-bit rows need warps more than loads in flight (4900 tokens of 20 key heads,
+// appended and read back: six CTAs an SM 31 us, five 33, four 35.6; one row group
+// loaded at a time: 34 with six); 16-bit rows are at the memory's rate with five.
 template <typename ACT, int D, bool U4, bool INTER>
-__global__ void __launch_bounds__(kRowThreads, 5) paged_append_kernel(const PagedAppendArgs a, int subs, int iters) {
+__global__ void __launch_bounds__(kRowThreads, U4 ? 6 : 5) paged_append_kernel(const PagedAppendArgs a, int subs, int iters) {
   constexpr int LPR = D / 16;    // lanes per row
   constexpr int RPI = 32 / LPR;  // rows a warp holds at once
   constexpr int U = U4 ? 2 : 4;  // row groups loaded together
