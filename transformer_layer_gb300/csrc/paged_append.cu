@@ -25,10 +25,10 @@
 // the quantiser issued 221 instructions per two rows and ran at half the
 // bandwidth.)
 //
-// Measured: 24 prompts, 32 query and 8 key heads, 16-bit pages, appended and
-// read back: 63 us, 6.5 TB/s (98 % of a copy).  4-bit pages are bound by issue
+// Measured: 24 prompts, 32 query and 8 key heads, 16-bit pages, appended:
+// 63 us, 6.5 TB/s (98 % of a copy).  4-bit pages are bound by issue
 // (about 190 instructions per four rows, most of them the quantiser's): 7
-// prompts, 20 heads, 31 us, 3.6 TB/s.
+// prompts, 20 heads, appended and read back: 31 us, 3.6 TB/s.
 #include "paged.cuh"
 
 namespace ds {
