@@ -163,3 +163,42 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i, x in got:
         assert torch.equal(x, ref if i == 2 else ref_p)
+
+
+def test_u4_values_that_average_out_over_a_long_cache():
+    """200 thousand 4-bit rows around zero: the sums over codes and over minima are
+    hundreds of times their difference, the result.  What is left of it is the rounding of
+    the output and of each weight (fp16, acting on scale * (code - 8)): independent, each
+    at most half a step and so 2^-11 / sqrt(3) of its value in the root mean square.
+    A tenth is allowed for the fp32 sums."""
+    N, nk, G, d, page = 200000, 8, 2, 128, 64
+    n_pages = -(-N // page)
+    g = gen(13)
+    k, v = (torch.randint(0, 256, (n_pages, nk, page, d // 2), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2))
+    scale = torch.rand((n_pages, nk, page, 1), generator=g, device="cuda") * 0.1 + 0.3
+    sc = torch.cat([scale, -7.5 * scale], -1).half()
+    table = torch.randperm(n_pages, generator=torch.Generator().manual_seed(3))
+    c = ds.paged_cache(k, v, table.int().cuda()[None].contiguous(), F16, sc, sc)
+    q = randn((1, nk * G, d), g, F16) * 0.3
+    nb = ds.ds_paged_attention_workspace_bytes(c, nk * G, 1, 1)
+    ws, out = new_workspace(nb), torch.empty_like(q)
+    ds.ds_paged_attention(c, q, out, i32([N - 1]), 1, 1, ws, nb)
+    status_ok(ws)
+    order = table.cuda()
+
+    def rows(codes, h):  # codes, scales and minima of a head's positions, in 64 bits
+        x = codes[order, h].reshape(-1, d // 2)[:N]
+        s = sc[order, h].reshape(-1, 2)[:N].double()
+        return torch.stack([x & 15, x >> 4], -1).reshape(N, d).double(), s[:, :1], s[:, 1:]
+
+    err, allowed = 0.0, 0.0
+    for h in range(nk):
+        kc, ks, km = rows(k, h)
+        vc, vs, vm = rows(v, h)
+        for i in range(G):
+            p = torch.softmax((kc * ks + km) @ q[0, h * G + i].double() * d ** -0.5, 0)
+            ref = p @ (vc * vs + vm)
+            weights = (p * p) @ (vs * (vc - 8)) ** 2
+            err += ((out[0, h * G + i].double() - ref) ** 2).sum().item()
+            allowed += (2.0 ** -22 / 3 * (ref ** 2 + weights)).sum().item()
+    assert err <= 1.1 ** 2 * allowed, (err / allowed) ** 0.5
