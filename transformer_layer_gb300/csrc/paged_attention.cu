@@ -49,8 +49,8 @@
 // 6.2 TB/s (94 % of a copy).  4-bit pages are bound by the unpacking's
 // instructions and their latency (about 250 per 16 positions, 0.49 issued a cycle
 // and scheduler; 16 warps an SM in 128 registers were no faster): 2 sequences of 90 to
-// 131 thousand positions 60 us, 4.0 TB/s; 96 of 300 to 6000 42 us, 2.4 TB/s.  One
-// sequence of 545 positions, 32 heads: 11.5 us, half of it the chain of look-ups,
+// 131 thousand positions 54 us, 4.5 TB/s; 96 of 300 to 6000 42 us, 2.4 TB/s.  One
+// sequence of 545 positions, 32 heads: 10.7 us, half of it the chain of look-ups,
 // first loads and the join.
 #include <math.h>
 
@@ -745,35 +745,77 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
       __syncthreads();
       if (s_last) {
         if (tid == 0) pl.counters[first] = 0;
-        for (int i = tid; i < RP * (D / 4); i += kPaThreads) {
-          const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-          float M = -INFINITY, L = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k0 = first; k0 <= last; k0 += 4) {
-            float mk[4], lk[4];
-            float4 x[4];
+        // 32 parts at a time: a lane's part and a warp's rows give the weights, then a
+        // thread sums its channels over the parts, 16 loads on their way together (28 parts a
+        // segment: 60 -> 54 us for the call against four of them and a running maximum)
+        constexpr int ITEMS = RP * (D / 4) / kPaThreads, AHEAD = 16 / ITEMS;
+        auto slot_of = [&](int k) { return ((size_t)k * 2 + (k == first ? 1 : 0)) * RP; };
+        float* s_w = reinterpret_cast<float*>(sm);  // [row][32]; (O of the warps has gone into the part)
+        float *s_top = s_m[0], *s_sum = s_l[0], *s_old = s_m[1];  // maximum, sum, weight of the earlier parts
+        float4 v[ITEMS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // four parts' loads on their way together
-              const int k = min(k0 + i, last);
-              const size_t at = ((size_t)k * 2 + (k == first ? 1 : 0)) * RP + r;
-              mk[i] = ld_cg(pl.part_ml + at * 2);
-              lk[i] = ld_cg(pl.part_ml + at * 2 + 1);
-              x[i] = ld_cg4(pl.part_o + at * D + c);
+        for (int x = 0; x < ITEMS; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = first; k0 <= last; k0 += 32) {
+          const int n = min(32, last - k0 + 1);
+#pragma unroll
+          for (int x = 0; x < RP / kPaWarps; ++x) {
+            const int r = warp + x * kPaWarps;
+            float m1 = -INFINITY, l1 = 0.f;
+            if (lane < n) {
+              const float* ml = pl.part_ml + (slot_of(k0 + lane) + r) * 2;
+              m1 = ld_cg(ml);
+              l1 = ld_cg(ml + 1);
             }
+            const float before = k0 == first ? -INFINITY : s_top[r];
+            float top = fmaxf(before, m1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (k0 + i > last || (mk[i] == -INFINITY && lk[i] == 0.f)) continue;
-              const float mn = fmaxf(M, mk[i]), f0 = ex2(M - mn), f1 = ex2(mk[i] - mn);
-              L = L * f0 + lk[i] * f1;
-              v.x = v.x * f0 + x[i].x * f1;
-              v.y = v.y * f0 + x[i].y * f1;
-              v.z = v.z * f0 + x[i].z * f1;
-              v.w = v.w * f0 + x[i].w * f1;
-              M = mn;
+            for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            // (a part without positions holds nothing; one with NaN scores only keeps them)
+            const float w = m1 == -INFINITY ? l1 : ex2(m1 - top);
+            float sum = w * l1;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            s_w[r * 32 + lane] = w;
+            __syncwarp();
+            if (lane == 0) {
+              const float old = before == -INFINITY ? 0.f : ex2(before - top);
+              s_sum[r] = k0 == first ? sum : fmaf(s_sum[r], before == -INFINITY ? 1.f : old, sum);
+              s_top[r] = top;
+              s_old[r] = old;
             }
           }
-          const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-          store(r, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+          __syncthreads();
+#pragma unroll
+          for (int x = 0; x < ITEMS; ++x) {
+            const float old = s_old[(tid + x * kPaThreads) / (D / 4)];
+            if (k0 > first && old != 1.f) v[x] = make_float4(v[x].x * old, v[x].y * old, v[x].z * old, v[x].w * old);
+          }
+          for (int k = 0; k < n; k += AHEAD) {
+            float4 y[AHEAD][ITEMS];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+              for (int x = 0; x < ITEMS; ++x)
+                y[i][x] = ld_cg4(pl.part_o + slot_of(k0 + min(k + i, n - 1)) * D + (size_t)(tid + x * kPaThreads) * 4);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+              for (int x = 0; x < ITEMS; ++x) {
+                const float w = s_w[(tid + x * kPaThreads) / (D / 4) * 32 + min(k + i, n - 1)];
+                if (k + i >= n || w == 0.f) continue;
+                v[x].x = fmaf(w, y[i][x].x, v[x].x);
+                v[x].y = fmaf(w, y[i][x].y, v[x].y);
+                v[x].z = fmaf(w, y[i][x].z, v[x].z);
+                v[x].w = fmaf(w, y[i][x].w, v[x].w);
+              }
+          }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int x = 0; x < ITEMS; ++x) {
+          const int i = tid + x * kPaThreads, r = i / (D / 4);
+          const float L = s_sum[r], inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+          store(r, (i % (D / 4)) * 4, make_float4(v[x].x * inv, v[x].y * inv, v[x].z * inv, v[x].w * inv));
         }
       }
     }
