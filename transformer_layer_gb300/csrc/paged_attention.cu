@@ -41,16 +41,17 @@
 //
 // Split: a segment is (sequence, key head, group of 8 or 16 rows), its length
 // known on the device only.  Every CTA takes the same number of 16-position
-// blocks of the segments laid end to end (two CTAs per SM), whatever the
+// blocks of the segments laid end to end (two CTAs per SM, 4-bit three; a segment
+// itself counts as some blocks, pa_segment), whatever the
 // lengths; a segment that crosses CTAs leaves partial sums in the workspace,
 // and the last CTA to arrive joins them in order (the same bits every time).
 //
-// Measured: 48 sequences of 700 to 8192 positions, 8 key heads, bf16 pages: 97 us,
-// 6.2 TB/s (94 % of a copy).  4-bit pages are bound by the unpacking's
-// instructions and their latency (about 250 per 16 positions, 0.49 issued a cycle
-// and scheduler; 16 warps an SM in 128 registers were no faster): 2 sequences of 90 to
-// 131 thousand positions 54 us, 4.5 TB/s; 96 of 300 to 6000 42 us, 2.4 TB/s.  One
-// sequence of 545 positions, 32 heads: 10.7 us, half of it the chain of look-ups,
+// Measured: 48 sequences of 700 to 8192 positions, 8 key heads, bf16 pages: 96 us,
+// 6.3 TB/s (95 % of a copy).  4-bit pages are bound by the unpacking's
+// instructions and their latency (about 250 per 16 positions, half of them issued at
+// the ALU's rate; 16 warps an SM in 128 registers were no faster): 2 sequences of 90 to
+// 131 thousand positions 53 us, 4.6 TB/s; 96 of 300 to 6000 33 us, 3.0 TB/s.  One
+// sequence of 545 positions, 32 heads: 8.1 us, most of it the chain of look-ups,
 // first loads and the join.
 #include <math.h>
 
@@ -162,7 +163,8 @@ struct PaTile {
 };
 
 // Where a launch's blocks lie: segments (b, key head, row group) end to end,
-// sequence b having `per_b` segments of nb(b) blocks each.
+// sequence b having `per_b` segments of nb(b) blocks each, counted as
+// pa_segment units more.
 struct PaPlan {
   int nrt = 1;          // row groups per (sequence, key head)
   int min_chunk = 4;    // blocks a CTA takes at least
@@ -177,12 +179,20 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
 }
 __device__ __forceinline__ int pa_blocks(const PagedAttnArgs& a, int b) { return max(1, (pa_len(a, b) + 15) >> 4); }
 
+// Units of a segment besides its blocks: what its start, the merge of its warps and
+// its join cost, in blocks.  Measured (16-bit pages: one sequence of 545 positions,
+// five of 200 to 1500, 48 of 700 to 8192) 0: 11.4, 12.4, 98.5 us; 6: 10.5, 12.7, 95.8; 16:
+// 8.6, 9.6, 96.1; 32: 9.0, 9.8, 94.8.  (4-bit: 96 of 300 to 6000, 2 of 90 to 131 thousand)
+// 0: 42.9, 55.1; 16: 35.9, 53.9; 32: 33.4, 52.7; 64: 35.7, 53.3; 128: 40.8, 54.4.
+__host__ __device__ constexpr int pa_segment(bool u4) { return u4 ? 32 : 16; }
+
 template <typename ACT, int D, bool U4, int NR>
 __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
     paged_attention_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ PaPlan pl) {
   using Tile = PaTile<D, U4>;
   constexpr int KB = Tile::KB, NST = Tile::NST, ROW = Tile::ROW;
   constexpr int RP = 8 * NR;    // rows of a segment
+  constexpr int SEG = pa_segment(U4);
   constexpr int MT = D / 16;    // 16-channel tiles of O^T
   constexpr int KS = D / 16;    // 16-channel steps of S^T
   constexpr int OS = D + 4;     // row stride of the merge buffer: conflict-free
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
     long long sum = 0;
     unsigned over = 0;
     for (int b = b0; b < b1; ++b) {
-      sum += (long long)pa_blocks(a, b) * per_b;
+      sum += (long long)(pa_blocks(a, b) + SEG) * per_b;
       if (a.past[b] > (a.c.table_stride << a.c.page_shift) - a.T) over = kFlagCacheOverflow;
     }
     if (over != 0 && blockIdx.x == 0) atomicOr(a.status, over);
@@ -234,7 +244,7 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
       long long at = lo;
       int b = b0;
       for (;; ++b) {
-        const long long n = (long long)pa_blocks(a, b) * per_b;
+        const long long n = (long long)(pa_blocks(a, b) + SEG) * per_b;
         if (c_lo < at + n || b + 1 >= b1) break;
         at += n;
       }
@@ -245,15 +255,16 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
   }
   int b = (int)s_first[1];
   int nb = pa_blocks(a, b);
-  int seg = (int)((c_lo - s_first[0]) / nb);  // of sequence b
-  long long seg_lo = s_first[0] + (long long)seg * nb;
+  int seg = (int)((c_lo - s_first[0]) / (nb + SEG));                     // of sequence b
+  long long seg_lo = s_first[0] + (long long)seg * (nb + SEG) + SEG;  // the unit of its first block
   unsigned bad = 0;
   unsigned holes = 0;  // bit slot * KB + j: block j of the tile in that stage is not attended
 
   for (long long cur = c_lo; cur < c_hi;) {
     // ---- segment (b, kh, rt): blocks [k0, k1) are this CTA's
     const int kh = seg / pl.nrt, rt = seg - kh * pl.nrt;
-    const int k0 = (int)(cur - seg_lo), k1 = (int)min((long long)nb, c_hi - seg_lo);
+    const int k0 = (int)max(0LL, cur - seg_lo), k1 = (int)min((long long)nb, c_hi - seg_lo);
+    if (k1 <= 0) break;  // the share ends before the segment's first block
     const int len = pa_len(a, b), past = min(a.past[b], a.c.table_stride << a.c.page_shift);
     const int ntile = (k1 - k0 + KB - 1) / KB;  // tiles; warp w takes w, w + kPaWarps, ...
     const int32_t* table = a.c.table + (size_t)b * a.c.table_stride;
@@ -823,7 +834,7 @@ __global__ void __launch_bounds__(kPaThreads, pa_ctas(U4, NR))
 
     // ---- the next segment
     cur = seg_hi;
-    seg_lo = seg_hi;
+    seg_lo = seg_hi + SEG;
     if (++seg == per_b) {
       seg = 0;
       if (++b < B) nb = pa_blocks(a, b);
@@ -838,13 +849,11 @@ struct PaWs {
   size_t part_o, part_ml, total;
   int nr, nrt, grid, min_chunk;
 };
-// Blocks of 16 positions a CTA takes at least: one 64-position tile a warp of
-// 4-bit pages; two of the smaller tiles of 16-bit ones (one sequence of 545
-// positions, 32 heads: 11.7 us against 13.0 with one, joining more parts, and
-// 11.9 with three).
+// Units a CTA takes at least: the blocks of one tile a warp (one sequence of 545
+// positions, 32 heads of 16-bit pages: 8.1 us; two tiles 8.6, four 10.2).
 static int pa_min_chunk(const PagedView& c) {
   if (c.u4) return kPaWarps * (c.head_dim == 64 ? PaTile<64, true>::KB : PaTile<128, true>::KB);
-  return 2 * kPaWarps * (c.head_dim == 64 ? PaTile<64, false>::KB : PaTile<128, false>::KB);
+  return kPaWarps * (c.head_dim == 64 ? PaTile<64, false>::KB : PaTile<128, false>::KB);
 }
 static PaWs pa_ws(const PagedView& c, int heads, int batch, int T, int num_sms) {
   PaWs w;
