@@ -201,3 +201,11 @@ def test_binding_checks_its_tensors():
                 lambda: ds.ds_paged_gather(c, k[0], k[0], table[0], table[0].long(), 1, table)):
         with pytest.raises((ValueError, KeyError)):
             bad()
+
+
+def test_append_needs_a_place_for_q():
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
+    c = ds.paged_cache(k, k.clone(), torch.zeros(2, 2, dtype=torch.int32), torch.float16)
+    rows, cu = torch.zeros(3, 2, 64, dtype=torch.float16), torch.tensor([0, 1, 3], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ds.ds_paged_append(c, rows, rows, rows, None, cu, cu, 2, None, torch.zeros(256, dtype=torch.uint8))

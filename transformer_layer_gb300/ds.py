@@ -504,6 +504,8 @@ def ds_paged_append(cache, q, k, v, q_out, cu_seqlens, past_len, batch, rotary, 
     heads = qs = qos = 0
     qp = qop = None
     if q is not None:
+        if q_out is None:
+            raise ValueError("q needs a q_out (q itself to rotate it in place)")
         heads = q.shape[1]
         qp, qs = _packed(q, dt, heads, d, "q")
         qop, qos = _packed(q_out, dt, heads, d, "q_out")
